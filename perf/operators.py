@@ -1,0 +1,441 @@
+"""The operators around the MoE layer that keep its training state in 8 bits, as cases to measure.
+
+Four operators, with their plain form in elementary torch operations:
+
+  norm      RMSNorm of x + residual, with the sum, the normalised rows in bf16 and in 8 bits with scales
+  norm_bwd  its gradients: to the rows (with the residual stream's own gradient added) and to the weight
+  fwd       the MoE layer (router, dispatch, grouped SwiGLU MLP, combine) that saves what its backward
+            needs in 8 bits: x by token, and the gate and up values by routed row
+  bwd       the layer's backward from that 8-bit state: dx, dW_gate_up, dW_down, dprob
+
+The 8-bit format: blocks of 32 consecutive columns of a row share a scale 2^e, the smallest power of
+two (e from -124 to 120) with max|v| <= 448 * 2^e over the block; a value is v / 2^e rounded to the
+nearest E4M3 (ties to even). The scale is stored as the byte e + 127. The last block of a row may be
+shorter. A value read back is (E4M3 value) * 2^e, which bf16 holds exactly. The gate half and the up
+half of a row have blocks of their own.
+"""
+import math
+
+import torch
+
+own = False
+
+BLOCK = 32
+EPS = 1e-6
+
+
+# ------------------------------------------------------------------ cases
+def _norm(name, T, H, residual):
+    return {"name": name, "op": "norm", "T": T, "H": H, "residual": residual}
+
+
+def _norm_bwd(name, T, H, dsum):
+    return {"name": name, "op": "norm_bwd", "T": T, "H": H, "dsum": dsum}
+
+
+def _layer(name, op, T, H, I, E, k, sigmoid=False, dead=0):
+    return {"name": name, "op": op, "T": T, "H": H, "I": I, "E": E, "k": k, "sigmoid": sigmoid, "dead": dead}
+
+
+def listed():
+    return [
+        # one decoded token in front of the layer: nothing but latency
+        _norm("norm one token", 1, 2048, True),
+        # a small batch of an odd size, rows that are no whole number of blocks, first layer (no residual)
+        _norm("norm ragged", 1003, 1000, False),
+        # a training batch at the Qwen3-30B-A3B width
+        _norm("norm qwen3", 4096, 2048, True),
+        # the largest: a long batch at the Llama-4 width, several times the L2 cache
+        _norm("norm llama4 long", 16384, 5120, True),
+        # the norm's backward in the Qwen3-30B-A3B step, first layer: no gradient from a residual stream
+        _norm_bwd("norm_bwd qwen3", 4096, 2048, False),
+        # the same at the Llama-4 width, inside the network
+        _norm_bwd("norm_bwd llama4", 8192, 5120, True),
+        # a small fine-tuning batch: 64 tokens over 128 experts, bound by reading the weights
+        _layer("fwd small", "fwd", 64, 2048, 768, 128, 8, dead=16),
+        # the forward of the Qwen3-30B-A3B training step
+        _layer("fwd qwen3", "fwd", 4096, 2048, 768, 128, 8),
+        # the forward of the Mixtral-8x7B shape: few large experts
+        _layer("fwd mixtral", "fwd", 4096, 4096, 14336, 8, 2),
+        # the smallest step: a unit test's layer, an odd number of tokens, launches only
+        _layer("bwd tiny", "bwd", 61, 128, 256, 8, 2, dead=1),
+        # the backward of the Qwen3-30B-A3B training step
+        _layer("bwd qwen3", "bwd", 4096, 2048, 768, 128, 8),
+        # the backward of the Llama-4-17Bx16E routed experts (sigmoid scores, one expert a token)
+        _layer("bwd llama4", "bwd", 8192, 5120, 8192, 16, 1, sigmoid=True),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["norm", "norm_bwd", "fwd", "fwd", "bwd", "bwd"])
+    if op in ("norm", "norm_bwd"):
+        H = 8 * _log(rng, 8, 1024)
+        T = _log(rng, 1, min(32768, 16384 * 5120 // H))
+        c = _norm("", T, H, rng.random() < 0.7) if op == "norm" else _norm_bwd("", min(T, 8192 * 5120 // H), H, rng.random() < 0.7)
+    else:
+        while True:
+            H, I = 8 * _log(rng, 8, 640), 8 * _log(rng, 8, 1024)
+            E = _log(rng, 1, 128)
+            k = rng.randint(1, min(E, 8))
+            T = _log(rng, 1, 8192)
+            # no dearer than the largest listed: its weights and its products (blocks padded to the fullest expert)
+            if E * H * I <= 16 * 5120 * 8192 and T * k * H * I <= 8192 * 5120 * 8192 // 4 and T * k * (H + 2 * I) <= 4e8:
+                break
+        dead = rng.randint(0, (E - k) // 2)
+        c = _layer("", op, T, H, I, E, k, rng.random() < 0.3, dead)
+    del c["name"]
+    return c
+
+
+# ------------------------------------------------------------------ inputs
+def _pow2(e):
+    """2^e in float32 for whole e in [-126, 127], exactly."""
+    return ((e.to(torch.int32) + 127) << 23).view(torch.float32)
+
+
+def _encode(v, width):
+    """(E4M3 bytes, exponents) of float32 rows v [R, parts * width], blocks of 32 inside each width."""
+    R, n = v.shape
+    parts, S = n // width, -(-width // BLOCK)
+    b = torch.nn.functional.pad(v.reshape(R, parts, width), (0, S * BLOCK - width)).reshape(R, parts * S, BLOCK)
+    m, ex = torch.frexp(b.abs().amax(dim=2))                     # amax = m 2^ex, 448 = 0.875 * 2^9
+    e = (ex - 9 + (m > 0.875).to(ex.dtype)).clamp(-124, 120)
+    q = (b * _pow2(-e)[:, :, None]).to(torch.float8_e4m3fn)
+    q = q.view(torch.uint8).reshape(R, parts, S * BLOCK)[:, :, :width].reshape(R, n)
+    return q.contiguous(), e
+
+
+def _decode(q, e, width):
+    """float32 values of E4M3 bytes q [R, parts * width] with exponents e [R, parts * S]."""
+    R, n = q.shape
+    parts, S = n // width, -(-width // BLOCK)
+    scale = _pow2(e).reshape(R, parts, S, 1).expand(R, parts, S, BLOCK).reshape(R, parts, S * BLOCK)[:, :, :width]
+    return q.view(torch.float8_e4m3fn).float() * scale.reshape(R, n)
+
+
+def _route(c, g):
+    """Router logits with mild skew and `dead` experts that no token wants."""
+    T, E = c["T"], c["E"]
+    bias = 0.3 * torch.randn(E, generator=g, device="cuda")
+    order = torch.randperm(E, generator=g, device="cuda")
+    bias = torch.where(order < c["dead"], torch.full_like(bias, -1e4), bias)
+    return torch.randn(T, E, generator=g, device="cuda") + bias
+
+
+def _dispatch(logits, c):
+    """The router's outputs: choices, weights, counts, offsets, rows (stable by expert), all on the device."""
+    T, E, k = c["T"], c["E"], c["k"]
+    best, idx = torch.sort(logits, dim=1, descending=True, stable=True)   # ties: the lower expert first
+    best, idx = best[:, :k], idx[:, :k]
+    prob = torch.sigmoid(best) if c["sigmoid"] else torch.softmax(best, dim=1)
+    flat = idx.reshape(-1)
+    order = torch.sort(flat, stable=True)[1]                              # flat assignment of each row
+    row_of = torch.empty_like(order)
+    row_of[order] = torch.arange(T * k, device=logits.device)
+    counts = torch.zeros(E, dtype=torch.int64, device=logits.device).index_add_(0, flat, torch.ones_like(flat))
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int64, device=logits.device), counts.cumsum(0)])
+    return idx, prob, counts, offsets, row_of.reshape(T, k), order
+
+
+def prepare(case, seed):
+    c = case
+    g = torch.Generator(device="cuda")
+    g.manual_seed(int(seed) * 1000003 + 17)
+
+    def normal(*shape, std=1.0):
+        return torch.randn(*shape, generator=g, device="cuda") * std
+
+    def bf(t):
+        return t.to(torch.bfloat16)
+
+    s = {"case": c}
+    if c["op"] in ("norm", "norm_bwd"):
+        T, H = c["T"], c["H"]
+        # a residual stream: channels of unequal size, a few of them large, rows of unequal length
+        channel = torch.exp(0.5 * normal(H)) * (1 + 20 * (torch.rand(H, generator=g, device="cuda") < 0.002))
+        rows = torch.exp(0.3 * normal(T, 1))
+        s["weight"] = bf(1 + 0.2 * normal(H))
+        if c["op"] == "norm":
+            s["x"] = bf(normal(T, H))
+            s["residual"] = bf(normal(T, H) * channel * rows) if c["residual"] else None
+        else:
+            s["h"] = bf(normal(T, H) * channel * rows)
+            s["rstd"] = torch.rsqrt(s["h"].float().square().mean(dim=1) + EPS)
+            s["dy"] = bf(normal(T, H, std=0.01))
+            s["dsum"] = bf(normal(T, H, std=0.01)) if c["dsum"] else None
+        return s
+    T, H, I, E, k = c["T"], c["H"], c["I"], c["E"], c["k"]
+    s["w_gate_up"] = torch.empty(E, H, 2 * I, dtype=torch.bfloat16, device="cuda")
+    s["w_down"] = torch.empty(E, I, H, dtype=torch.bfloat16, device="cuda")
+    for e in range(E):   # expert by expert: no float32 copy of all weights
+        s["w_gate_up"][e] = normal(H, 2 * I, std=H ** -0.5)
+        s["w_down"][e] = normal(I, H, std=I ** -0.5)
+    s["logits"] = _route(c, g)
+    if c["op"] == "fwd":
+        s["x"] = bf(normal(T, H))
+        return s
+    # the state that a forward pass leaves, in the layouts of the layer
+    idx, prob, counts, offsets, row_of, order = _dispatch(s["logits"], c)
+    x_q, x_e = _encode(normal(T, H), H)
+    gu_q, gu_e = _encode(normal(T * k, 2 * I), I)
+    s["state"] = {"topk_prob": prob.contiguous(), "offsets": offsets.to(torch.int32), "row_of": row_of.to(torch.int32).contiguous(),
+                  "x_q": x_q, "x_scale": (x_e + 127).to(torch.uint8).contiguous(),
+                  "gu_q": gu_q, "gu_scale": (gu_e + 127).to(torch.uint8).t().contiguous()}
+    s["fullest"] = int(counts.max())   # the plain form's rows per expert
+    s["dout"] = bf(normal(T, H))
+    return s
+
+
+# ------------------------------------------------------------------ one pass
+def run(state):
+    op = state["case"]["op"]
+    if own:
+        return {"norm": _own_norm, "norm_bwd": _own_norm_bwd, "fwd": _own_fwd, "bwd": _own_bwd}[op](state)
+    return {"norm": _plain_norm, "norm_bwd": _plain_norm_bwd, "fwd": _plain_fwd, "bwd": _plain_bwd}[op](state)
+
+
+def _own_norm(s):
+    import routing_grouped_gemm_score_b200 as moe
+    r = moe.moe_rmsnorm(s["x"], s["weight"], EPS, residual=s["residual"], quantize=True)
+    y8 = moe.moe_dequantize_rows(r["y_q"], r["y_scale"])
+    out = {"y": r["y"], "rstd": r["rstd"], "y8": y8}
+    if s["residual"] is not None:
+        out["sum"] = r["sum"]
+    return out
+
+
+def _own_norm_bwd(s):
+    import routing_grouped_gemm_score_b200 as moe
+    r = moe.moe_rmsnorm_backward(s["dy"], s["h"], s["weight"], s["rstd"], dsum=s["dsum"])
+    return {"dx": r["dx"], "dweight": r["dweight"]}
+
+
+def _own_fwd(s):
+    import routing_grouped_gemm_score_b200 as moe
+    c = s["case"]
+    opts = moe.RouterOpts(moe.SCORE_SIGMOID, renormalize=False) if c["sigmoid"] else moe.RouterOpts()
+    out, st = moe.moe_layer_forward_ckpt8(s["logits"], s["x"], s["w_gate_up"], s["w_down"], c["k"], opts)
+    x8 = moe.moe_dequantize_rows(st["x_q"], st["x_scale"])
+    gu8 = moe.moe_dequantize_rows(st["gu_q"], st["gu_scale"], parts=2, block_major=True)
+    return {"out": out, "topk_idx": st["topk_idx"], "topk_prob": st["topk_prob"], "offsets": st["offsets"],
+            "row_of": st["row_of"], "x8": x8, "gu8": gu8}
+
+
+def _own_bwd(s):
+    import routing_grouped_gemm_score_b200 as moe
+    r = moe.moe_grouped_mlp_backward_ckpt8(s["dout"], s["state"], s["w_gate_up"], s["w_down"])
+    return {"dx": r["dx"], "dw_gate_up": r["dw_gate_up"], "dw_down": r["dw_down"], "dprob": r["dprob"]}
+
+
+def _plain_norm(s):
+    x, w = s["x"], s["weight"].float()
+    out = {}
+    h = x
+    if s["residual"] is not None:
+        h = (x.float() + s["residual"].float()).to(torch.bfloat16)   # the stored sum is what is normalised
+        out["sum"] = h
+    h = h.float()
+    rstd = torch.rsqrt(h.square().mean(dim=1) + EPS)
+    y = h * rstd[:, None] * w
+    H = y.shape[1]
+    q, e = _encode(y, H)
+    out.update(y=y.to(torch.bfloat16), rstd=rstd, y8=_decode(q, e, H).to(torch.bfloat16))
+    return out
+
+
+def _plain_norm_bwd(s):
+    h, w, dy, rstd = s["h"].float(), s["weight"].float(), s["dy"].float(), s["rstd"][:, None]
+    xhat = h * rstd
+    wdy = w * dy
+    dx = rstd * (wdy - xhat * (wdy * xhat).mean(dim=1, keepdim=True))
+    if s["dsum"] is not None:
+        dx = dx + s["dsum"].float()
+    return {"dx": dx.to(torch.bfloat16), "dweight": (dy * xhat).sum(dim=0)}
+
+
+def _blocks(offsets, counts, fullest, A):
+    """Row of every slot [E, fullest] of the experts' blocks, and which slots hold one."""
+    slot = torch.arange(fullest, device=offsets.device)
+    have = slot[None, :] < counts[:, None]
+    return (offsets[:-1, None] + slot[None, :]).clamp(max=A - 1), have
+
+
+def _plain_fwd(s):
+    c = s["case"]
+    T, I, k = c["T"], c["I"], c["k"]
+    A = T * k
+    idx, prob, counts, offsets, row_of, order = _dispatch(s["logits"], c)
+    rows, have = _blocks(offsets, counts, int(counts.max()), A)
+    x = s["x"].float()
+    gu_b = torch.bmm(x[order[rows] // k], s["w_gate_up"].float())     # [E, fullest, 2I]
+    h = gu_b[:, :, :I] * torch.sigmoid(gu_b[:, :, :I]) * gu_b[:, :, I:]
+    y_b = torch.bmm(h, s["w_down"].float())
+    gu, y = gu_b[have], y_b[have]                                     # the slots that hold rows, in row order
+    out = (prob[:, :, None] * y[row_of]).sum(dim=1)
+    x_q, x_e = _encode(x, x.shape[1])
+    gu_q, gu_e = _encode(gu, I)
+    return {"out": out.to(torch.bfloat16), "topk_idx": idx.to(torch.int32), "topk_prob": prob,
+            "offsets": offsets.to(torch.int32), "row_of": row_of.to(torch.int32),
+            "x8": _decode(x_q, x_e, x.shape[1]).to(torch.bfloat16), "gu8": _decode(gu_q, gu_e, I).to(torch.bfloat16)}
+
+
+def _plain_bwd(s):
+    c, st = s["case"], s["state"]
+    T, I, k = c["T"], c["I"], c["k"]
+    A = T * k
+    offsets, row_of = st["offsets"].long(), st["row_of"].long()
+    rows, have = _blocks(offsets, offsets[1:] - offsets[:-1], s["fullest"], A)
+    order = torch.empty(A, dtype=torch.int64, device=rows.device)
+    order[row_of.reshape(-1)] = torch.arange(A, device=rows.device)
+    p = st["topk_prob"].reshape(-1)[order]
+    x = _decode(st["x_q"], st["x_scale"].int() - 127, c["H"])
+    gu = _decode(st["gu_q"], st["gu_scale"].t().int() - 127, I)
+    dy = s["dout"].float()[order[rows] // k] * have[:, :, None]
+    w_down = s["w_down"].float()
+    dh = torch.bmm(dy, w_down.transpose(1, 2))                        # [E, fullest, I], before the weight p
+    g, u = gu[rows][:, :, :I], gu[rows][:, :, I:]
+    sg = torch.sigmoid(g)
+    h = g * sg * u
+    dprob = (dh * h).sum(dim=2)[have][row_of]
+    ds = p[rows][:, :, None] * dh
+    dgu = torch.cat([ds * u * (sg + g * sg * (1 - sg)), ds * g * sg], dim=2)
+    dw_down = torch.bmm((p[rows][:, :, None] * h).transpose(1, 2), dy)
+    del w_down, dh, ds
+    dw_gate_up = torch.bmm(x[order[rows] // k].transpose(1, 2), dgu)
+    dx = torch.bmm(dgu, s["w_gate_up"].float().transpose(1, 2))[have][row_of].sum(dim=1)
+    return {"dx": dx.to(torch.bfloat16), "dw_gate_up": dw_gate_up.to(torch.bfloat16),
+            "dw_down": dw_down.to(torch.bfloat16), "dprob": dprob}
+
+
+# ------------------------------------------------------------------ what a pass cannot do without
+def work(case):
+    c = case
+    T, H = c["T"], c["H"]
+    scales = T * -(-H // BLOCK)
+    if c["op"] == "norm":
+        rows = T * H * 2 * (2 if c["residual"] else 1)                     # x, residual
+        rows += T * H * 2 * (2 if c["residual"] else 1) + T * H + scales   # sum, y, y in 8 bits
+        return {"bytes": rows + 2 * H + 4 * T, "flops": 8 * T * H}
+    if c["op"] == "norm_bwd":
+        return {"bytes": T * H * 2 * (4 if c["dsum"] else 3) + 6 * H + 4 * T, "flops": 12 * T * H}
+    I, E, k = c["I"], c["E"], c["k"]
+    A = T * k
+    experts = min(E - c["dead"], A)
+    ckpt = T * H + scales + A * 2 * I + A * 2 * -(-I // BLOCK)             # the 8-bit state
+    if c["op"] == "fwd":
+        weights = experts * 3 * H * I * 2
+        return {"bytes": weights + 4 * T * E + 2 * T * H * 2 + ckpt + 12 * A, "flops": 6 * A * H * I}
+    weights = experts * 3 * H * I * 2 + E * 3 * H * I * 2                  # read, and every gradient written
+    return {"bytes": weights + 2 * T * H * 2 + ckpt + 12 * A, "flops": 12 * A * H * I}
+
+
+# ------------------------------------------------------------------ the definition in 64 bits
+def _round8(v, width):
+    """float64 rows with every value replaced by the 8-bit value that stands for it, as bf16."""
+    out = torch.empty_like(v)
+    for part in range(v.shape[1] // width):
+        for c0 in range(0, width, BLOCK):
+            cols = slice(part * width + c0, part * width + min(c0 + BLOCK, width))
+            b = v[:, cols]
+            a = b.abs().amax(dim=1, keepdim=True)
+            e = torch.ceil(torch.log2(a / 448.0)).clamp(-124.0, 120.0)     # a = 0: log2 is -inf, e = -124
+            e = torch.where(a > 448.0 * torch.exp2(e), e + 1, e)           # log2 near a whole number
+            e = torch.where((a <= 224.0 * torch.exp2(e)) & (e > -124), e - 1, e)
+            t = b / torch.exp2(e)
+            step = torch.exp2(torch.floor(torch.log2(t.abs().clamp(min=2.0 ** -6))) - 3)
+            out[:, cols] = torch.round(t / step) * step * torch.exp2(e)
+    return out.to(torch.bfloat16)
+
+
+def _sig(v):
+    return 1.0 / (1.0 + torch.exp(-v))
+
+
+def exact(case, seed):
+    c, s = case, prepare(case, seed)
+    T, H = c["T"], c["H"]
+    if c["op"] == "norm":
+        h = s["x"].double()
+        out = {}
+        if s["residual"] is not None:
+            out["sum"] = (h + s["residual"].double()).to(torch.bfloat16)
+            h = out["sum"].double()
+        rstd = 1.0 / torch.sqrt((h * h).sum(dim=1) / H + EPS)
+        y = torch.einsum("th,t,h->th", h, rstd, s["weight"].double())
+        out.update(y=y, rstd=rstd, y8=_round8(y, H))
+        return out
+    if c["op"] == "norm_bwd":
+        h, w, dy, r = s["h"].double(), s["weight"].double(), s["dy"].double(), s["rstd"].double()
+        inner = torch.einsum("th,th,h->t", dy, h, w)
+        dx = r[:, None] * w * dy - (r ** 3 * inner / H)[:, None] * h
+        if s["dsum"] is not None:
+            dx += s["dsum"].double()
+        return {"dx": dx, "dweight": torch.einsum("th,th,t->h", dy, h, r)}
+    I, E, k = c["I"], c["E"], c["k"]
+    A = T * k
+    if c["op"] == "fwd":
+        logits = s["logits"].double()
+        left, prob = s["logits"].clone(), torch.zeros(T, k, dtype=torch.float64, device="cuda")
+        idx = torch.empty(T, k, dtype=torch.int64, device="cuda")
+        place = torch.arange(E, device="cuda")
+        for j in range(k):   # the best expert left, the lowest index among equals
+            top = left.amax(dim=1, keepdim=True)
+            idx[:, j] = torch.where(left == top, place, torch.full_like(place, E)).amin(dim=1)
+            left.scatter_(1, idx[:, j:j + 1], -math.inf)
+        chosen = torch.gather(logits, 1, idx)
+        prob = _sig(chosen) if c["sigmoid"] else torch.exp(chosen - torch.logsumexp(chosen, dim=1, keepdim=True))
+        out = torch.zeros(T, H, dtype=torch.float64, device="cuda")
+        gu = torch.empty(A, 2 * I, dtype=torch.float64, device="cuda")
+        row_of = torch.empty(T, k, dtype=torch.int64, device="cuda")
+        offsets = [0]
+        for e in range(E):
+            tok, j = torch.nonzero(idx == e, as_tuple=True)
+            a, b = offsets[-1], offsets[-1] + tok.numel()
+            offsets.append(b)
+            if a == b:
+                continue
+            row_of[tok, j] = torch.arange(a, b, device="cuda")
+            gu[a:b] = s["x"][tok].double() @ s["w_gate_up"][e].double()
+            g, u = gu[a:b].split(I, dim=1)
+            out.index_add_(0, tok, prob[tok, j][:, None] * ((g * _sig(g) * u) @ s["w_down"][e].double()))
+        return {"out": out, "topk_idx": idx.to(torch.int32), "topk_prob": prob,
+                "offsets": torch.tensor(offsets, dtype=torch.int32, device="cuda"), "row_of": row_of.to(torch.int32),
+                "x8": _round8(s["x"].double(), H), "gu8": _round8(gu, I)}
+    st = s["state"]
+
+    def values(q, byte, width):   # E4M3: sign, 4 exponent bits (bias 7), 3 fraction bits
+        q = q.to(torch.int32)
+        ex, fr = ((q >> 3) & 15).double(), (q & 7).double()
+        v = torch.where(ex > 0, (1 + fr / 8) * torch.exp2(ex - 7), fr / 8 * 2.0 ** -6)
+        v = torch.where(q >= 128, -v, v)
+        S = -(-width // BLOCK)
+        col = torch.arange(q.shape[1], device="cuda")
+        block = (col // width) * S + (col % width) // BLOCK
+        return v * torch.exp2(byte.double() - 127)[:, block]
+
+    x, gu, dout = values(st["x_q"], st["x_scale"], H), values(st["gu_q"], st["gu_scale"].t(), I), s["dout"].double()
+    dx = torch.zeros(T, H, dtype=torch.float64, device="cuda")
+    dprob = torch.zeros(T, k, dtype=torch.float64, device="cuda")
+    dw_gate_up = torch.zeros(E, H, 2 * I, dtype=torch.float64, device="cuda")
+    dw_down = torch.zeros(E, I, H, dtype=torch.float64, device="cuda")
+    off = st["offsets"].tolist()
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        if a == b:
+            continue
+        tok, j = torch.nonzero((st["row_of"] >= a) & (st["row_of"] < b), as_tuple=True)
+        at = st["row_of"][tok, j].long()
+        g, u, p = gu[at, :I], gu[at, I:], st["topk_prob"][tok, j].double()[:, None]
+        sg = _sig(g)
+        act = g * sg * u
+        d = dout[tok] @ s["w_down"][e].double().t()
+        dprob[tok, j] = (d * act).sum(dim=1)
+        dw_down[e] = (p * act).t() @ dout[tok]
+        dz = torch.cat([p * d * u * sg * (1 + g * (1 - sg)), p * d * g * sg], dim=1)
+        dw_gate_up[e] = x[tok].t() @ dz
+        dx.index_add_(0, tok, dz @ s["w_gate_up"][e].double().t())
+    return {"dx": dx, "dw_gate_up": dw_gate_up, "dw_down": dw_down, "dprob": dprob}
