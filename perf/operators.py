@@ -218,7 +218,7 @@ def _own_fwd(s):
     import routing_grouped_gemm_score_b200 as moe
     c = s["case"]
     opts = moe.RouterOpts(moe.SCORE_SIGMOID, renormalize=False) if c["sigmoid"] else moe.RouterOpts()
-    out, st = moe.moe_layer_forward_ckpt8(s["logits"], s["x"], s["w_gate_up"], s["w_down"], c["k"], opts)
+    out, st = moe.moe_layer_forward_ckpt(s["logits"], s["x"], s["w_gate_up"], s["w_down"], c["k"], opts)
     x8 = moe.moe_dequantize_rows(st["x_q"], st["x_scale"])
     gu8 = moe.moe_dequantize_rows(st["gu_q"], st["gu_scale"], parts=2, block_major=True)
     return {"out": out, "topk_idx": st["topk_idx"], "topk_prob": st["topk_prob"], "offsets": st["offsets"],
@@ -227,7 +227,7 @@ def _own_fwd(s):
 
 def _own_bwd(s):
     import routing_grouped_gemm_score_b200 as moe
-    r = moe.moe_grouped_mlp_backward_ckpt8(s["dout"], s["state"], s["w_gate_up"], s["w_down"])
+    r = moe.moe_grouped_mlp_backward_ckpt(s["dout"], s["state"], s["w_gate_up"], s["w_down"])
     return {"dx": r["dx"], "dw_gate_up": r["dw_gate_up"], "dw_down": r["dw_down"], "dprob": r["dprob"]}
 
 
