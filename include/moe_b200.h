@@ -105,6 +105,77 @@ moe_status moe_get_device_status(void* stream);
  * not thread-safe. Returns MOE_ERR_INVALID_ARG if n_events < 0. */
 moe_status moe_trace_set(void* const* events, int n_events);
 
+/* --------------------------------------------------------- 8-bit row format
+ * The format of moe_rmsnorm's 8-bit output and of the layer's 8-bit training
+ * state (moe_layer_forward_ckpt). A row of `cols` columns is cut into blocks
+ * of 32 consecutive columns (the last may be shorter), S = ceil(cols / 32) of
+ * them. With a the largest finite magnitude of a block,
+ *   e = the smallest integer with a <= 448 * 2^e, held to [-124, 120],
+ * stored as the byte e + 127, and each value is stored as v * 2^-e rounded to
+ * the nearest E4M3 (ties to even). The error of a value is at most 2^-4 of it,
+ * or 2^-10 * 2^e where it is small (at e = 120 values are held to 240 * 2^120,
+ * the largest that bf16 holds). A value read back, (E4M3 value) * 2^e, is
+ * exactly a bf16 value. Infinities and NaNs are stored as NaN and do not count
+ * towards a. A row may consist of two parts of `cols` columns each ([g | u]),
+ * whose blocks are separate. Scale bytes are [rows][parts * S], or, when
+ * block_major is 1, [parts * S][rows].
+ * moe_quantize_rows and moe_dequantize_rows convert rows of bf16 and back.
+ *  x      bf16  [rows, parts * cols]
+ *  q      uint8 [rows, parts * cols]   E4M3
+ *  scale  uint8 [rows, parts * S] or [parts * S, rows]; the values read back are
+ *         defined for scale bytes 1..254
+ * cols is a multiple of 8, at most 2^24; parts is 1 or 2; rows < 2^31. rows = 0
+ * is allowed. */
+moe_status moe_quantize_rows(const moe_bf16* x, int64_t rows, int cols, int parts, int block_major,
+                             uint8_t* q, uint8_t* scale, void* stream);
+moe_status moe_dequantize_rows(const uint8_t* q, const uint8_t* scale, int64_t rows, int cols,
+                               int parts, int block_major, moe_bf16* x, void* stream);
+
+/* ------------------------------------------------------------------ RMSNorm
+ * moe_rmsnorm -- the root-mean-square norm in front of the layer, with the
+ * residual's addition and an output in 8 bits. Per row, in fp32:
+ *   s = bf16(x + residual)   (s = x without a residual)
+ *   rstd = (sum_i s_i^2 / H + eps)^(-1/2)        y_i = s_i * rstd * weight_i
+ * The stored sum is what is normalised, so moe_rmsnorm_backward, which reads it,
+ * differentiates exactly this function, and the call gives the bits of a call
+ * without residual on that sum. y is stored in bf16 and, rounded once from the
+ * same fp32 value, in 8 bits (the format above, one part, scales by row): the
+ * x_q and x_scale of moe_layer_forward_ckpt.
+ *  x         in  bf16 [T, H]
+ *  residual  in  bf16 [T, H] (NULL: none)
+ *  weight    in  bf16 [H]
+ *  eps       >= 0; with eps = 0 a row of zeros gives NaN, as the formula does
+ *  sum       out bf16 [T, H], s (NULL: not stored; needs a residual). May be x
+ *            or residual itself
+ *  y         out bf16 [T, H] (NULL: not stored). May be x itself
+ *  y_q       out uint8 [T, H], y_scale out uint8 [T, ceil(H / 32)] (both NULL: not
+ *            stored; one of y and y_q is needed)
+ *  rstd      out fp32 [T] (NULL: not stored)
+ * H is a multiple of 8, at most 16384 (MOE_ERR_UNSUPPORTED otherwise); T = 0 is
+ * allowed. A row whose sum of squares passes fp32's range gets rstd = 0. */
+moe_status moe_rmsnorm(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* weight, int64_t T,
+                       int H, float eps, moe_bf16* sum, moe_bf16* y, uint8_t* y_q, uint8_t* y_scale,
+                       float* rstd, void* stream);
+
+/* moe_rmsnorm_backward -- gradients of moe_rmsnorm's y with respect to its row
+ * and its weight, from the forward's stored sum s (x without a residual) and
+ * rstd. With xhat = s * rstd, in fp32:
+ *   dx_i = rstd * (weight_i dy_i - xhat_i * sum_j weight_j dy_j xhat_j / H) + dsum_i
+ *   dweight_i = sum_t dy[t,i] * xhat[t,i]
+ * x and residual enter s alike, so dx is the gradient of both. dsum is the
+ * gradient that reaches s by its other use, the residual stream (NULL: none).
+ *  dy    in  bf16 [T, H]; s in bf16 [T, H]; weight in bf16 [H]; rstd in fp32 [T]
+ *  dsum  in  bf16 [T, H] (NULL: none)
+ *  dx    out bf16 [T, H]; may be dy or dsum itself
+ *  dweight out fp32 [H] (NULL: not computed, and no workspace needed)
+ *  workspace of moe_rmsnorm_backward_workspace_size(T, H) bytes, 16-byte aligned
+ * The sums over the rows run in a fixed order, so dweight is the same on every
+ * run on a given GPU. T = 0 gives dweight = 0. */
+size_t moe_rmsnorm_backward_workspace_size(int64_t T, int H);
+moe_status moe_rmsnorm_backward(const moe_bf16* dy, const moe_bf16* s, const moe_bf16* weight,
+                                const float* rstd, const moe_bf16* dsum, int64_t T, int H, moe_bf16* dx,
+                                float* dweight, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------------ router
  * moe_router_topk -- TE Router (fused_topk_with_score_function); te_mixtral.py
  * TEMixtralSparseMoeBlock.forward (fp32 softmax, top-k, renormalise).
@@ -434,6 +505,64 @@ moe_status moe_grouped_mlp_scaled_backward(const moe_bf16* dout, int64_t T, int 
                                            moe_bf16* dx, moe_bf16* dw_gate_up, moe_bf16* dw_down,
                                            float* dprob, void* workspace, size_t workspace_bytes,
                                            void* stream);
+
+/* ------------------------------------------- training state in 8 bits
+ * moe_layer_forward_ckpt -- moe_layer_forward that keeps, for
+ * moe_grouped_mlp_backward_ckpt, an 8-bit state in place of the bf16 one: x by
+ * token and [g | u] by routed row in the 8-bit row format. h, y_perm and x_perm
+ * are not kept. Per routed row that is 2I bytes (and a k-th of H), against
+ * 4H + 6I. out and the routing are those of moe_layer_forward, bit for bit: only
+ * what is saved is rounded, g and u once, from the fp32 accumulators.
+ *  topk_idx, topk_prob, offsets, row_of  out, as in moe_layer_forward (needed)
+ *  counts    out int32 [E] (NULL: not returned)
+ *  x_given   0: x_q and x_scale are written from x. 1: the caller has them
+ *            (moe_rmsnorm's y_q and y_scale); they are not touched and may be NULL
+ *  x_q       out uint8 [T, H], x_scale out uint8 [T, ceil(H / 32)]
+ *  gu_q      out uint8 [A, 2I]: two parts of I columns
+ *  gu_scale  out uint8 [2 ceil(I / 32), A]: block-major
+ * Other arguments, limits and the workspace (moe_layer_forward_workspace_size) as
+ * in moe_layer_forward. */
+moe_status moe_layer_forward_ckpt(const float* logits, const moe_bf16* x, int64_t T, int H, int I,
+                                   int E, int k, const moe_router_opts* opts,
+                                   const moe_bf16* w_gate_up, const moe_bf16* w_down,
+                                   const moe_bf16* shared_gate_up, const moe_bf16* shared_down,
+                                   moe_bf16* out, int32_t* topk_idx, float* topk_prob, int32_t* counts,
+                                   int32_t* offsets, int32_t* row_of, uint8_t* x_q, uint8_t* x_scale,
+                                   int x_given, uint8_t* gu_q, uint8_t* gu_scale, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* moe_grouped_mlp_backward_ckpt -- moe_grouped_mlp_backward from the 8-bit state.
+ * With x, g and u the values that the state stands for, a = silu(g) * u, and
+ * row = row_of[t,j], p = topk_prob[t,j]:
+ *   dh = dout[t] . w_down[e]^T        dprob[t,j] = <dh, a[row]>
+ *   ds = p * dh     du = ds * silu(g)     dg = ds * u * silu'(g)
+ *   dx[t] = sum_j [dg | du] . w_gate_up[e]^T
+ *   dw_down[e] = (p a)_e^T . dout_e   dw_gate_up[e] = x_e^T . [dg | du]_e
+ * (the same gradients: the weight p is applied to the activation's side, so dout
+ * enters the products unrounded and y_perm is not needed). Accumulation is fp32;
+ * p a, [dg | du] and each row's dx are rounded to bf16, the tensor cores' operand
+ * type. dprob sums 64-column groups in column order, then the groups in order,
+ * so it is the same on every run. An expert with no rows gets zero weight
+ * gradients; T = 0 gives zero weight gradients.
+ * The stages recorded by moe_trace_set are:
+ *   [0] start  [1] dout by row  [2] down dgrad + SwiGLU backward  [3] down wgrad
+ *   [4] gate_up dgrad  [5] token sum of dx  [6] x by row + gate_up wgrad
+ *  row_of, topk_prob, offsets, x_q, x_scale, gu_q, gu_scale  in, from
+ *      moe_layer_forward_ckpt (x_q and x_scale possibly from moe_rmsnorm)
+ *  dout in bf16 [T,H]; dx out bf16 [T,H]; dw_gate_up out bf16 [E,H,2I];
+ *  dw_down out bf16 [E,I,H]; dprob out fp32 [T,k];
+ *  workspace of moe_grouped_mlp_backward_ckpt_workspace_size(T, H, I, E, k) bytes,
+ *  16-byte aligned. A row index outside [0, T k) is recorded as
+ *  MOE_ERR_DEVICE_CHECK and its assignment skipped. */
+size_t moe_grouped_mlp_backward_ckpt_workspace_size(int64_t T, int H, int I, int E, int k);
+moe_status moe_grouped_mlp_backward_ckpt(const moe_bf16* dout, int64_t T, int H, int I, int E, int k,
+                                          const moe_bf16* w_gate_up, const moe_bf16* w_down,
+                                          const int32_t* row_of, const float* topk_prob,
+                                          const int32_t* offsets, const uint8_t* x_q,
+                                          const uint8_t* x_scale, const uint8_t* gu_q,
+                                          const uint8_t* gu_scale, moe_bf16* dx, moe_bf16* dw_gate_up,
+                                          moe_bf16* dw_down, float* dprob, void* workspace,
+                                          size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------ testing hooks
  * moe_testing_set_kernels -- forces one kernel variant for every later call in

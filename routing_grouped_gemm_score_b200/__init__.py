@@ -11,7 +11,10 @@ Stages (Transformer Engine "Mixture of Experts": Router, Token dispatch,
 Grouped MLP, Token combine):
     moe_router_topk -> moe_permute -> moe_grouped_mlp -> moe_unpermute_combine
 fused as moe_layer_forward, with moe_grouped_mlp_backward for training and
-moe_router_backward for the gradient through the score function.
+moe_router_backward for the gradient through the score function. With
+moe_layer_forward_ckpt and moe_grouped_mlp_backward_ckpt the state kept for the
+backward is in 8 bits; moe_rmsnorm, the norm in front of the layer, can write the
+layer's x in that format as well.
 """
 from __future__ import annotations
 
@@ -28,6 +31,8 @@ __all__ = [
     "moe_grouped_mlp", "moe_unpermute_combine", "moe_layer_forward", "moe_grouped_mlp_backward",
     "moe_grouped_mlp_scaled_backward",
     "moe_trace_set", "moe_router_topk_noalloc", "moe_router_backward", "moe_expert_bias_update", "LayerWorkspace", "ABI_FUNCTIONS",
+    "moe_quantize_rows", "moe_dequantize_rows", "moe_rmsnorm", "moe_rmsnorm_backward",
+    "moe_layer_forward_ckpt", "moe_grouped_mlp_backward_ckpt",
 ]
 
 SCORE_SOFTMAX = 0
@@ -105,6 +110,16 @@ ABI_FUNCTIONS = {
     "moe_grouped_mlp_scaled_backward_workspace_size": (SZ, [I64, I32, I32]),
     "moe_grouped_mlp_scaled_backward": (I32, [P, I64, I32, I32, I32, I32, P, P, P, P, P, P, I64, P, P, P,
                                               P, P, P, P, P, SZ, P]),
+    "moe_quantize_rows": (I32, [P, I64, I32, I32, I32, P, P, P]),
+    "moe_dequantize_rows": (I32, [P, P, I64, I32, I32, I32, P, P]),
+    "moe_rmsnorm": (I32, [P, P, P, I64, I32, F32, P, P, P, P, P, P]),
+    "moe_rmsnorm_backward_workspace_size": (SZ, [I64, I32]),
+    "moe_rmsnorm_backward": (I32, [P, P, P, P, P, I64, I32, P, P, P, SZ, P]),
+    "moe_layer_forward_ckpt": (I32, [P, P, I64, I32, I32, I32, I32, ctypes.POINTER(_RouterOptsC), P, P, P,
+                                      P, P, P, P, P, P, P, P, P, I32, P, P, P, SZ, P]),
+    "moe_grouped_mlp_backward_ckpt_workspace_size": (SZ, [I64, I32, I32, I32, I32]),
+    "moe_grouped_mlp_backward_ckpt": (I32, [P, I64, I32, I32, I32, I32, P, P, P, P, P, P, P, P, P, P, P, P,
+                                             P, P, SZ, P]),
     "moe_testing_set_kernels": (I32, [I32, I32, I32, I32]),
     "moe_testing_wait_timeout": (I32, [I64, P]),
 }
@@ -157,6 +172,27 @@ def _need(t: torch.Tensor, dtype, name: str) -> None:
         raise ValueError(f"{name} must be on a CUDA device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _need_shape(t: torch.Tensor, dtype, shape: tuple, name: str) -> None:
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _on_device(tensors):
+    """The CUDA device that all given tensors (None is skipped) are on, as a
+    context in which it is the current one, so that the call takes that device's
+    current stream and its kernels run there."""
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"tensors on different devices: {device} and {t.device}")
+    return torch.cuda.device(device)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -460,13 +496,16 @@ def moe_unpermute_combine_rows(y_perm: torch.Tensor, row_of: torch.Tensor,
 
 class LayerWorkspace:
     """A reusable workspace for moe_layer_forward / moe_grouped_mlp_backward,
-    sized once for a shape, so repeated calls allocate nothing."""
+    sized once for a shape, so repeated calls allocate nothing. With ckpt the
+    backward part is moe_grouped_mlp_backward_ckpt's."""
 
-    def __init__(self, T, H, I, E, k, has_shared=False, backward=False, device="cuda"):
+    def __init__(self, T, H, I, E, k, has_shared=False, backward=False, device="cuda", ckpt=False):
         n = lib().moe_layer_forward_workspace_size(T, H, I, E, k, int(has_shared))
         self.fwd = _workspace(n, device)
-        self.bwd = None
-        if backward:
+        self.bwd = self.bwd8 = None
+        if backward and ckpt:
+            self.bwd8 = _workspace(lib().moe_grouped_mlp_backward_ckpt_workspace_size(T, H, I, E, k), device)
+        elif backward:
             self.bwd = _workspace(lib().moe_grouped_mlp_backward_workspace_size(T, H, I, E, k), device)
 
 
@@ -587,3 +626,248 @@ def moe_grouped_mlp_scaled_backward(dout: torch.Tensor, row_of: torch.Tensor, so
         _ptr(grads["dw_gate_up"]), _ptr(grads["dw_down"]), _ptr(grads["dprob"]), _ptr(ws), ws.numel(),
         _stream()), "moe_grouped_mlp_scaled_backward")
     return grads
+
+
+# ------------------------------------------------------- 8-bit rows, RMSNorm
+ROWS8_BLOCK = 32   # columns that share a scale
+
+
+def _rows8_shape(q: torch.Tensor, parts: int, block_major: bool) -> tuple:
+    """(rows, cols of a part, shape of the scales) of rows [..., parts * cols]."""
+    if q.dim() != 2:
+        raise ValueError(f"rows must have two dimensions, got {tuple(q.shape)}")
+    if parts not in (1, 2):
+        raise ValueError(f"parts must be 1 or 2, got {parts}")
+    rows, width = q.shape
+    if width % parts:
+        raise ValueError(f"{width} columns do not divide into {parts} parts")
+    cols = width // parts
+    blocks = parts * -(-cols // ROWS8_BLOCK)
+    return rows, cols, (blocks, rows) if block_major else (rows, blocks)
+
+
+def moe_quantize_rows(x: torch.Tensor, parts: int = 1, block_major: bool = False) -> tuple:
+    """(q, scale): bf16 rows in the 8-bit format, E4M3 bytes (uint8, x's shape)
+    and a scale byte per 32 columns, [rows, blocks] or, block_major,
+    [blocks, rows]."""
+    _need(x, torch.bfloat16, "x")
+    rows, cols, scale_shape = _rows8_shape(x, parts, block_major)
+    with _on_device([x]):
+        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        scale = torch.empty(scale_shape, dtype=torch.uint8, device=x.device)
+        _check(lib().moe_quantize_rows(_ptr(x), rows, cols, parts, int(block_major), _ptr(q), _ptr(scale), _stream()),
+               "moe_quantize_rows")
+    return q, scale
+
+
+def moe_dequantize_rows(q: torch.Tensor, scale: torch.Tensor, parts: int = 1, block_major: bool = False,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The bf16 values (exact) that rows in the 8-bit format stand for. A layer
+    state's [g | u]: moe_dequantize_rows(state["gu_q"], state["gu_scale"], parts=2,
+    block_major=True)."""
+    _need(q, torch.uint8, "q")
+    rows, cols, scale_shape = _rows8_shape(q, parts, block_major)
+    _need_shape(scale, torch.uint8, scale_shape, "scale")
+    if out is not None:
+        _need_shape(out, torch.bfloat16, q.shape, "out")
+    with _on_device([q, scale, out]):
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        _check(lib().moe_dequantize_rows(_ptr(q), _ptr(scale), rows, cols, parts, int(block_major), _ptr(out),
+                                         _stream()), "moe_dequantize_rows")
+    return out
+
+
+def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                quantize: bool = False, out: Optional[dict] = None) -> dict:
+    """RMSNorm of x + residual [T, H]: a dict with y (bf16), sum (x + residual in
+    bf16; x itself without a residual), rstd (fp32 [T]) and, with quantize, y_q and
+    y_scale, y in the 8-bit format (the x8 of moe_layer_forward_ckpt). sum and
+    rstd are what moe_rmsnorm_backward needs. `out`: preallocated tensors by those
+    names ("sum" may be x or residual itself, for an update in place); what it does
+    not hold is allocated, except that an entry that is None is not computed (sum,
+    rstd, or y next to the 8-bit output)."""
+    _need(x, torch.bfloat16, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must have two dimensions, got {tuple(x.shape)}")
+    T, H = x.shape
+    _need_shape(weight, torch.bfloat16, (H,), "weight")
+    if residual is not None:
+        _need_shape(residual, torch.bfloat16, (T, H), "residual")
+    want = {"y": (torch.bfloat16, (T, H)), "rstd": (torch.float32, (T,))}
+    if residual is not None:
+        want["sum"] = (torch.bfloat16, (T, H))
+    if quantize:
+        want["y_q"] = (torch.uint8, (T, H))
+        want["y_scale"] = (torch.uint8, (T, -(-H // ROWS8_BLOCK)))
+    given = dict(out or {})
+    for name in given:
+        if name not in want:
+            raise ValueError(f"out: this call does not write {name!r}")
+    with _on_device([x, weight, residual, *given.values()]):
+        r = {}
+        for name, (dtype, shape) in want.items():
+            if name not in given:
+                r[name] = torch.empty(shape, dtype=dtype, device=x.device)
+            else:
+                r[name] = given[name]
+                if r[name] is not None:
+                    _need_shape(r[name], dtype, shape, name)
+        g = r.get
+        _check(lib().moe_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), T, H, float(eps), _ptr(g("sum")), _ptr(g("y")),
+                                 _ptr(g("y_q")), _ptr(g("y_scale")), _ptr(g("rstd")), _stream()), "moe_rmsnorm")
+    if residual is None:
+        r["sum"] = x
+    return r
+
+
+def moe_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                         dsum: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                         want_dweight: bool = True, workspace: Optional[torch.Tensor] = None) -> dict:
+    """{"dx", "dweight"} from the forward's "sum" and "rstd". dsum: the gradient that
+    reaches the sum by the residual stream, added to dx. dx may be given, also as dy
+    or dsum itself. dweight (fp32 [H]) is None with want_dweight False."""
+    _need(dy, torch.bfloat16, "dy")
+    if dy.dim() != 2:
+        raise ValueError(f"dy must have two dimensions, got {tuple(dy.shape)}")
+    T, H = dy.shape
+    _need_shape(s, torch.bfloat16, (T, H), "s")
+    _need_shape(weight, torch.bfloat16, (H,), "weight")
+    _need_shape(rstd, torch.float32, (T,), "rstd")
+    for t, n in ((dsum, "dsum"), (dx, "dx")):
+        if t is not None:
+            _need_shape(t, torch.bfloat16, (T, H), n)
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
+    with _on_device([dy, s, weight, rstd, dsum, dx, workspace]):
+        if dx is None:
+            dx = torch.empty((T, H), dtype=torch.bfloat16, device=dy.device)
+        dweight = torch.empty(H, dtype=torch.float32, device=dy.device) if want_dweight else None
+        if workspace is None and want_dweight:
+            workspace = _workspace(lib().moe_rmsnorm_backward_workspace_size(T, H), dy.device)
+        _check(lib().moe_rmsnorm_backward(_ptr(dy), _ptr(s), _ptr(weight), _ptr(rstd), _ptr(dsum), T, H, _ptr(dx),
+                                          _ptr(dweight), _ptr(workspace),
+                                          0 if workspace is None else workspace.numel(), _stream()),
+               "moe_rmsnorm_backward")
+    return {"dx": dx, "dweight": dweight}
+
+
+# --------------------------------------------------- training state in 8 bits
+def _layer_shapes(w_gate_up: torch.Tensor, w_down: torch.Tensor, H: int) -> tuple:
+    """(E, I) of a layer's expert weights, their shapes checked against H."""
+    _need(w_gate_up, torch.bfloat16, "w_gate_up")
+    _need(w_down, torch.bfloat16, "w_down")
+    if w_down.dim() != 3:
+        raise ValueError(f"w_down must be [E, I, H], got {tuple(w_down.shape)}")
+    E, I, _ = w_down.shape
+    _need_shape(w_down, torch.bfloat16, (E, I, H), "w_down")
+    _need_shape(w_gate_up, torch.bfloat16, (E, H, 2 * I), "w_gate_up")
+    return E, I
+
+
+def _ckpt_spec(T: int, H: int, I: int, E: int, k: int) -> dict:
+    """Types and shapes of the 8-bit layer state."""
+    A, block = T * k, ROWS8_BLOCK
+    return {
+        "topk_idx": (torch.int32, (T, k)), "topk_prob": (torch.float32, (T, k)), "counts": (torch.int32, (E,)),
+        "offsets": (torch.int32, (E + 1,)), "row_of": (torch.int32, (T, k)),
+        "x_q": (torch.uint8, (T, H)), "x_scale": (torch.uint8, (T, -(-H // block))),
+        "gu_q": (torch.uint8, (A, 2 * I)), "gu_scale": (torch.uint8, (2 * -(-I // block), A)),
+    }
+
+
+def moe_layer_forward_ckpt(logits: torch.Tensor, x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
+                            k: int, opts: Optional[RouterOpts] = None, shared_gate_up: Optional[torch.Tensor] = None,
+                            shared_down: Optional[torch.Tensor] = None, x8: Optional[tuple] = None,
+                            workspace: Optional[LayerWorkspace] = None, out: Optional[torch.Tensor] = None,
+                            state: Optional[dict] = None) -> tuple:
+    """moe_layer_forward that keeps its state for the backward in 8 bits:
+    (out, state), with state for moe_grouped_mlp_backward_ckpt. out and the
+    routing are those of moe_layer_forward. x8: (y_q, y_scale) of the moe_rmsnorm
+    that made x, which then enter the state as they are. `state`: the dict of an
+    earlier call of the same shape, written again (not its x_q and x_scale when x8
+    is given)."""
+    _need(logits, torch.float32, "logits")
+    _need(x, torch.bfloat16, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must have two dimensions, got {tuple(x.shape)}")
+    T, H = x.shape
+    E, I = _layer_shapes(w_gate_up, w_down, H)
+    _need_shape(logits, torch.float32, (T, E), "logits")
+    k = int(k)
+    if k < 1 or k > E:
+        raise ValueError(f"k must be in [1, {E}], got {k}")
+    if (shared_gate_up is None) != (shared_down is None):
+        raise ValueError("a shared expert needs both shared_gate_up and shared_down")
+    for t, shape, n in ((shared_gate_up, (H, 2 * I), "shared_gate_up"), (shared_down, (I, H), "shared_down")):
+        if t is not None:
+            _need(t, torch.bfloat16, n)
+            if tuple(t.shape) not in (shape, (1, *shape)):
+                raise ValueError(f"{n}: expected shape {shape}, got {tuple(t.shape)}")
+    opts = opts or RouterOpts()
+    if opts.expert_bias is not None:
+        _need_shape(opts.expert_bias, torch.float32, (E,), "expert_bias")
+    spec = _ckpt_spec(T, H, I, E, k)
+    st = dict(state or {})
+    if x8 is not None:
+        st["x_q"], st["x_scale"] = x8
+    for name, t in st.items():
+        if name in spec:
+            _need_shape(t, spec[name][0], spec[name][1], name)
+    if out is not None:
+        _need_shape(out, torch.bfloat16, (T, H), "out")
+    with _on_device([logits, x, w_gate_up, w_down, shared_gate_up, shared_down, out, opts.expert_bias,
+                     *[st[n] for n in spec if n in st], None if workspace is None else workspace.fwd]):
+        if out is None:
+            out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        for name, (dtype, shape) in spec.items():
+            if name not in st:
+                st[name] = torch.empty(shape, dtype=dtype, device=x.device)
+        if workspace is None:
+            workspace = LayerWorkspace(T, H, I, E, k, shared_gate_up is not None, device=x.device)
+        oc = opts.c()
+        _check(lib().moe_layer_forward_ckpt(
+            _ptr(logits), _ptr(x), T, H, I, E, k, ctypes.byref(oc), _ptr(w_gate_up), _ptr(w_down),
+            _ptr(shared_gate_up), _ptr(shared_down), _ptr(out), _ptr(st["topk_idx"]), _ptr(st["topk_prob"]),
+            _ptr(st["counts"]), _ptr(st["offsets"]), _ptr(st["row_of"]), _ptr(st["x_q"]), _ptr(st["x_scale"]),
+            int(x8 is not None), _ptr(st["gu_q"]), _ptr(st["gu_scale"]), _ptr(workspace.fwd), workspace.fwd.numel(),
+            _stream()), "moe_layer_forward_ckpt")
+    return out, st
+
+
+def moe_grouped_mlp_backward_ckpt(dout: torch.Tensor, state: dict, w_gate_up: torch.Tensor, w_down: torch.Tensor,
+                                   workspace: Optional[LayerWorkspace] = None, grads: Optional[dict] = None) -> dict:
+    """Gradients of the layer with respect to x, w_gate_up, w_down and the
+    routing weights, from the 8-bit state of moe_layer_forward_ckpt."""
+    _need(dout, torch.bfloat16, "dout")
+    if dout.dim() != 2:
+        raise ValueError(f"dout must have two dimensions, got {tuple(dout.shape)}")
+    T, H = dout.shape
+    E, I = _layer_shapes(w_gate_up, w_down, H)
+    s = state
+    if s["row_of"].dim() != 2:
+        raise ValueError(f"row_of must be [T, k], got {tuple(s['row_of'].shape)}")
+    k = s["row_of"].shape[1]
+    spec = _ckpt_spec(T, H, I, E, k)
+    used = ("row_of", "topk_prob", "offsets", "x_q", "x_scale", "gu_q", "gu_scale")
+    for name in used:
+        _need_shape(s[name], spec[name][0], spec[name][1], name)
+    want = {"dx": (torch.bfloat16, (T, H)), "dw_gate_up": (torch.bfloat16, (E, H, 2 * I)),
+            "dw_down": (torch.bfloat16, (E, I, H)), "dprob": (torch.float32, (T, k))}
+    g = dict(grads or {})
+    for name, (dtype, shape) in want.items():
+        if name in g:
+            _need_shape(g[name], dtype, shape, name)
+    ws = None if workspace is None else workspace.bwd8
+    with _on_device([dout, w_gate_up, w_down, ws, *[s[n] for n in used], *[g[n] for n in want if n in g]]):
+        for name, (dtype, shape) in want.items():
+            if name not in g:
+                g[name] = torch.empty(shape, dtype=dtype, device=dout.device)
+        if ws is None:
+            ws = _workspace(lib().moe_grouped_mlp_backward_ckpt_workspace_size(T, H, I, E, k), dout.device)
+        _check(lib().moe_grouped_mlp_backward_ckpt(
+            _ptr(dout), T, H, I, E, k, _ptr(w_gate_up), _ptr(w_down), _ptr(s["row_of"]), _ptr(s["topk_prob"]),
+            _ptr(s["offsets"]), _ptr(s["x_q"]), _ptr(s["x_scale"]), _ptr(s["gu_q"]), _ptr(s["gu_scale"]),
+            _ptr(g["dx"]), _ptr(g["dw_gate_up"]), _ptr(g["dw_down"]), _ptr(g["dprob"]), _ptr(ws), ws.numel(),
+            _stream()), "moe_grouped_mlp_backward_ckpt")
+    return g

@@ -55,6 +55,7 @@
 
 #include "moe_common.cuh"
 #include "moe_internal.h"
+#include "rows8.cuh"
 
 namespace moe {
 
@@ -80,7 +81,9 @@ constexpr int kStageHalfP = 64 * BK * 2 + kStageBP;
 
 // kEpiStoreAdd: the store with the token combine folded in (the shared
 // expert's down GEMM, whose output rows are the tokens in order).
-enum Epi { kEpiStore = 0, kEpiSwiglu = 1, kEpiSwigluBwd = 2, kEpiStoreAdd = 3 };
+// kEpiSwigluBwd8: the SwiGLU backward from g and u saved in 8 bits, which also
+// recomputes h for the weight gradient of the down GEMM.
+enum Epi { kEpiStore = 0, kEpiSwiglu = 1, kEpiSwigluBwd = 2, kEpiStoreAdd = 3, kEpiSwigluBwd8 = 4 };
 
 struct Params {
     int groups;           // number of experts
@@ -98,6 +101,12 @@ struct Params {
     int64_t ldo2;
     const bf16* aux;           // SwiGLU backward: the saved [g | u]
     int64_t ld_aux;
+    // [g | u] in 8 bits (rows8.cuh), written by the SwiGLU forward (NULL: skip)
+    // and read by kEpiSwigluBwd8: values [rows][2I], scale bytes [2 S][rows],
+    // S = ceil(I / 32), the blocks of g first. Block-major scales, because a
+    // lane holds a row: a warp's 32 bytes of one block are one sector.
+    uint8_t* gu8;
+    uint8_t* gu8_scale;
     int I;                     // SwiGLU: offset of the up half in [g | u]
     int tma_out, tma_out2;     // single-CTA kernel: out / out2 have TMA store maps
     const float* row_scale;    // SwiGLU forward: h[r] *= row_scale[r]; backward: ds = row_scale[r] * dh (NULL: 1)
@@ -385,6 +394,96 @@ __device__ __forceinline__ void load_aux32(const Params& p, int64_t grow, int co
     }
 }
 
+// Rounds a lane's 32 values (one block of its row, columns [0, ncols)) to 8 bits
+// and stores them at q (32 or ncols bytes) with their scale byte.
+__device__ __forceinline__ void store_block8(uint8_t* q, uint8_t* scale, int ncols, const float* v) {
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) a = fmaxf(a, i < ncols ? fabsf(v[i]) : 0.0f);   // a NaN does not count
+    uint32_t byte = rows8_scale_byte(a);
+    const bool special = a >= kRows8Special;
+    if (special) {
+        a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) a = fmaxf(a, i < ncols ? rows8_finite(v[i]) : 0.0f);
+        byte = rows8_scale_byte(a);
+    }
+    const float inv = rows8_inv_scale(byte);
+    *scale = (uint8_t)byte;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {   // 8-column pieces: rows are whole multiples of 8 bytes
+        if (8 * c >= ncols) break;
+        float s[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = special ? rows8_scaled_special(v[8 * c + i], byte) : v[8 * c + i] * inv;
+        *reinterpret_cast<uint2*>(q + 8 * c) =
+            make_uint2(rows8_pack4(s[0], s[1], s[2], s[3]), rows8_pack4(s[4], s[5], s[6], s[7]));
+    }
+}
+
+// The saved 8-bit g and u of one row for one block of 32 columns.
+struct Aux8 {
+    uint2 g[4], u[4];
+    uint32_t g_byte, u_byte;
+};
+
+// Loads a row's 8-bit g and u for the block of columns [col, col + 32) (col a
+// multiple of 32); does nothing when !ok. Issued a chunk ahead of use.
+__device__ __forceinline__ void load_aux8(const Params& p, int64_t grow, int col, bool ok, Aux8& a) {
+    if (!ok) return;
+    const uint8_t* row = p.gu8 + grow * 2 * p.I + col;
+    const uint8_t* sc = p.gu8_scale + (int64_t)(col / kRows8Block) * p.rows + grow;
+    a.g_byte = __ldg(sc);
+    a.u_byte = __ldg(sc + (int64_t)rows8_blocks(p.I) * p.rows);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const bool in = col + 8 * q < p.I;
+        a.g[q] = in ? __ldg(reinterpret_cast<const uint2*>(row) + q) : make_uint2(0, 0);
+        a.u[q] = in ? __ldg(reinterpret_cast<const uint2*>(row + p.I) + q) : make_uint2(0, 0);
+    }
+}
+
+// What an epilogue warp loads ahead of its accumulator.
+template <int EPI>
+struct EpiAux {
+    using type = Aux32;
+};
+template <>
+struct EpiAux<kEpiSwigluBwd8> {
+    using type = Aux8;
+};
+template <int EPI>
+__device__ __forceinline__ void load_epi_aux(const Params& p, int64_t grow, int col, bool ok,
+                                             typename EpiAux<EPI>::type& a) {
+    if constexpr (EPI == kEpiSwigluBwd8) load_aux8(p, grow, col, ok, a);
+    else load_aux32(p, grow, col, ok, a);
+}
+
+// SwiGLU backward of one block of 32 columns from the 8-bit g and u, with the
+// row's routing weight p: with a = silu(g) u and dh the gradient that reaches
+// p a (through the down GEMM, before the weight), dot gains sum dh a (the
+// gradient of p, in column order), dgp and dup get the bf16 dg and du of
+// ds = p dh, and hp the bf16 p a, the rows of the down weight's gradient.
+__device__ __forceinline__ void swiglu_bwd8(const float* dh, const Aux8& a, float p, float& dot, uint32_t* dgp,
+                                            uint32_t* dup, uint32_t* hp) {
+    const float gs = rows8_scale(a.g_byte), us = rows8_scale(a.u_byte);
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+        const uint2 gq = a.g[c / 8], uq = a.u[c / 8];
+        const uint32_t gw = ((c & 4) ? gq.y : gq.x) >> (8 * (c & 2)), uw = ((c & 4) ? uq.y : uq.x) >> (8 * (c & 2));
+        const float2 gf = rows8_unpack2(gw), uf = rows8_unpack2(uw);
+        const float g0 = gf.x * gs, g1 = gf.y * gs, u0 = uf.x * us, u1 = uf.y * us;
+        const float s0 = __frcp_rn(1.0f + expf(-g0)), s1 = __frcp_rn(1.0f + expf(-g1));
+        const float a0 = g0 * s0, a1 = g1 * s1;   // silu(g)
+        dot += dh[c] * (a0 * u0);
+        dot += dh[c + 1] * (a1 * u1);
+        const float d0 = p * dh[c], d1 = p * dh[c + 1];
+        hp[c / 2] = pack_bf16x2(p * (a0 * u0), p * (a1 * u1));
+        dup[c / 2] = pack_bf16x2(d0 * a0, d1 * a1);
+        dgp[c / 2] = pack_bf16x2(d0 * u0 * (s0 + a0 * (1.0f - s0)), d1 * u1 * (s1 + a1 * (1.0f - s1)));
+    }
+}
+
 // put_block32 for values already packed as bf16 pairs.
 __device__ __forceinline__ void put_block32_packed(uint8_t* buf, bf16* dst, int64_t ld, int nvalid, int ncols,
                                                    const uint32_t* w, int lane, const CUtensorMap* map, int x,
@@ -494,7 +593,7 @@ template <int EPI, bool GROUP_K>
 __device__ __forceinline__ void epilogue_tile(const Params& p, const Tile& t, uint32_t t_row,
                                               const EpiMap& em, int lane, int n_tile,
                                               uint8_t* buf, const CUtensorMap* tmC,
-                                              const CUtensorMap* tmC2, Aux32* pre) {
+                                              const CUtensorMap* tmC2, typename EpiAux<EPI>::type* pre) {
     const int warp_r0 = em.r0;
     const int r = warp_r0 + lane;
     if (EPI == kEpiSwiglu) {
@@ -519,11 +618,18 @@ __device__ __forceinline__ void epilogue_tile(const Params& p, const Tile& t, ui
                 put_block32(buf, p.out2 + row0 * p.ldo2 + p.I + n0 + c0, p.ldo2, nvalid, ncols, u, lane, tmC2,
                             p.I + n0 + c0, (int)row0);
             }
+            if (p.gu8 && lane < nvalid) {
+                // one rounding, from the fp32 accumulator
+                uint8_t* q = p.gu8 + (row0 + lane) * 2 * p.I + n0 + c0;
+                uint8_t* sc = p.gu8_scale + (int64_t)((n0 + c0) / kRows8Block) * p.rows + row0 + lane;
+                store_block8(q, sc, ncols, g);
+                store_block8(q + p.I, sc + (int64_t)rows8_blocks(p.I) * p.rows, ncols, u);
+            }
 #pragma unroll
             for (int i = 0; i < 32; ++i) g[i] = silu_f(g[i]) * u[i] * rs;     // h, in place
             put_block32(buf, p.out + row0 * p.ldo + n0 + c0, p.ldo, nvalid, ncols, g, lane, tmC, n0 + c0, (int)row0);
         }
-    } else if (EPI == kEpiSwigluBwd) {
+    } else if constexpr (EPI == kEpiSwigluBwd) {
         // the first chunk's g and u were loaded before the accumulator was
         // ready (`pre`); each later chunk's load while the one before is stored
         const int n0 = t.n_blk * n_tile;
@@ -563,6 +669,42 @@ __device__ __forceinline__ void epilogue_tile(const Params& p, const Tile& t, ui
             put_block32_packed(buf, p.out + row0 * p.ldo + col, p.ldo, nvalid, ncols, dgp, lane, tmC, col,
                                (int)row0);
             put_block32_packed(buf, p.out + row0 * p.ldo + p.I + col, p.ldo, nvalid, ncols, dup, lane, tmC, p.I + col,
+                               (int)row0);
+        }
+    } else if constexpr (EPI == kEpiSwigluBwd8) {
+        // as kEpiSwigluBwd, from the 8-bit g and u, with h stored as well (out2)
+        const int n0 = t.n_blk * n_tile;
+        const bool valid = r < t.rows;
+        const int nvalid = min(max(t.rows - warp_r0, 0), 32);
+        const int64_t grow = (int64_t)t.row0 + r;
+        const int64_t row0 = (int64_t)t.row0 + warp_r0;
+        Aux8& ax = *pre;
+        const float ps = valid ? __ldg(p.row_scale + grow) : 0.0f;
+        float dot = 0.0f;
+#pragma unroll 1
+        for (int ci = 0; ci < em.chunks; ++ci) {
+            const int col = n0 + em.c_lo + 32 * ci;
+            float dh[32];
+            tmem_load_32(t_row + (uint32_t)(em.tm + 32 * ci), dh);
+            if (col >= p.N) continue;
+            const int ncols = min(32, p.N - col);
+            uint32_t dgp[16], dup[16], hp[16];
+            if (valid) {
+                swiglu_bwd8(dh, ax, ps, dot, dgp, dup, hp);
+                if ((ci & 1) || col + 32 >= p.N) {   // the 64-column group's last chunk
+                    p.row_dot[grow * p.ld_row_dot + (col >> 6)] = dot;
+                    dot = 0.0f;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) dgp[i] = dup[i] = hp[i] = 0u;   // rows past the block: not stored
+            }
+            load_aux8(p, grow, col + 32, valid && ci + 1 < em.chunks && col + 32 < p.N, ax);
+            put_block32_packed(buf, p.out + row0 * p.ldo + col, p.ldo, nvalid, ncols, dgp, lane, tmC, col,
+                               (int)row0);
+            put_block32_packed(buf, p.out + row0 * p.ldo + p.I + col, p.ldo, nvalid, ncols, dup, lane, tmC, p.I + col,
+                               (int)row0);
+            put_block32_packed(buf, p.out2 + row0 * p.ldo2 + col, p.ldo2, nvalid, ncols, hp, lane, tmC2, col,
                                (int)row0);
         }
     } else if (GROUP_K) {
@@ -811,10 +953,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int buf = local_tile & 1;
             const uint32_t use = (uint32_t)(local_tile >> 1);
             const EpiMap em = t.rows <= 128 ? em_half : em_full;   // a copy: a reference would need memory
-            Aux32 pre;
-            if (EPI == kEpiSwigluBwd) {
+            typename EpiAux<EPI>::type pre;
+            if (EPI == kEpiSwigluBwd || EPI == kEpiSwigluBwd8) {
                 const int col = t.n_blk * BN + em.c_lo;
-                load_aux32(p, (int64_t)t.row0 + em.r0 + lane, col, em.r0 + lane < t.rows && col < p.N, pre);
+                load_epi_aux<EPI>(p, (int64_t)t.row0 + em.r0 + lane, col, em.r0 + lane < t.rows && col < p.N, pre);
             }
             if (!mbar_wait(&s.acc_full[buf], use & 1u, abort_flag, p.err)) break;
             tc_fence_after();
@@ -1095,10 +1237,10 @@ __global__ void __launch_bounds__(GROUP_K ? kThreadsK : kThreads, 1)
             const Tile t = decode_tile<GROUP_K>(s, p, id, BM1);
             const int buf = local_tile & 1;
             const uint32_t use = (uint32_t)(local_tile >> 1);
-            Aux32 pre;
-            if (EPI == kEpiSwigluBwd) {
+            typename EpiAux<EPI>::type pre;
+            if (EPI == kEpiSwigluBwd || EPI == kEpiSwigluBwd8) {
                 const int col = t.n_blk * BN + em.c_lo;
-                load_aux32(p, (int64_t)t.row0 + warp_r0 + lane, col, warp_r0 + lane < t.rows && col < p.N, pre);
+                load_epi_aux<EPI>(p, (int64_t)t.row0 + warp_r0 + lane, col, warp_r0 + lane < t.rows && col < p.N, pre);
             }
             if (!mbar_wait(&s.acc_full[buf], use & 1u, abort_flag, p.err)) break;
             tc_fence_after();
@@ -1256,6 +1398,26 @@ __device__ __forceinline__ bool swap_epi_swiglu(SmemS<NR>& s, const Params& p, c
     const int hc = t.n_blk * 64 + 32 * quarter + lane;   // column of h
     const float* urow = s.ubuf[buf][32 * quarter + lane] + j0;
     const int64_t r0 = (int64_t)t.row0 + j0;
+    if (p.gu8) {
+        // The warp's 32 lanes hold one block of 32 columns of every row. Its
+        // largest finite magnitude: bit patterns of non-negative floats order as
+        // the floats do, so an integer maximum over the warp finds it.
+        uint8_t* sc = p.gu8_scale + (int64_t)(t.n_blk * 2 + quarter) * p.rows + r0;
+#pragma unroll
+        for (int i = 0; i < kWC; ++i) {
+            if (i >= nvalid) break;   // the same for every lane
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const float x = hc < p.N ? (half == 0 ? v[i] : urow[i]) : 0.0f;
+                const uint32_t byte = rows8_scale_byte(
+                    __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(rows8_finite(x)))));
+                if (hc >= p.N) continue;
+                p.gu8[(r0 + i) * 2 * p.I + half * p.I + hc] =
+                    (uint8_t)(rows8_pack2(rows8_scaled_special(x, byte), 0.0f) & 0xFFu);
+                if (lane == 0) sc[(int64_t)half * rows8_blocks(p.I) * p.rows + i] = (uint8_t)byte;
+            }
+        }
+    }
 #pragma unroll
     for (int i = 0; i < kWC; ++i) {
         if (i >= nvalid || hc >= p.N) break;
@@ -1917,7 +2079,8 @@ bool make_out_map(CUtensorMap* m, const bf16* out, int64_t rows, uint64_t cols) 
 
 cudaError_t gemm_gate_up_swiglu(const bf16* x, int64_t rows, const int32_t* offsets, int E, int H,
                                 int I, const bf16* w_gate_up, bf16* h, bf16* gu_save,
-                                cudaStream_t st, unsigned* err, const float* row_scale, int64_t max_group_rows) {
+                                cudaStream_t st, unsigned* err, const float* row_scale, int64_t max_group_rows,
+                                const Rows8& gu8) {
     if (max_group_rows <= 0 || max_group_rows > rows) max_group_rows = rows;
     if (rows == 0) return cudaSuccess;
     CUtensorMap ta, ta64, tb;
@@ -1935,6 +2098,8 @@ cudaError_t gemm_gate_up_swiglu(const bf16* x, int64_t rows, const int32_t* offs
     p.ldo = I;
     p.out2 = gu_save;
     p.ldo2 = 2 * (int64_t)I;
+    p.gu8 = gu8.q;
+    p.gu8_scale = gu8.scale;
     p.row_scale = row_scale;
     if (use_swap_tiles(rows, groups)) {
         p.n_blocks = (I + 63) / 64;   // 64 gate and the matching 64 up columns per tile
@@ -1948,7 +2113,8 @@ cudaError_t gemm_gate_up_swiglu(const bf16* x, int64_t rows, const int32_t* offs
 
 cudaError_t gemm_gate_up_swiglu_gather(const bf16* x, int64_t T, const int32_t* sorted_token, int64_t rows,
                                        const int32_t* offsets, int E, int H, int I, const bf16* w_gate_up, bf16* h,
-                                       bf16* gu_save, cudaStream_t st, unsigned* err, const float* row_scale) {
+                                       bf16* gu_save, cudaStream_t st, unsigned* err, const float* row_scale,
+                                       const Rows8& gu8) {
     if (rows == 0) return cudaSuccess;
     if (H % 8 != 0 || (reinterpret_cast<uintptr_t>(x) & 15u) != 0 || !sorted_token || !offsets)
         return cudaErrorInvalidValue;
@@ -1965,6 +2131,8 @@ cudaError_t gemm_gate_up_swiglu_gather(const bf16* x, int64_t T, const int32_t* 
     p.ldo = I;
     p.out2 = gu_save;
     p.ldo2 = 2 * (int64_t)I;
+    p.gu8 = gu8.q;
+    p.gu8_scale = gu8.scale;
     p.row_scale = row_scale;
     p.gather_x = x;
     p.gather_tok = sorted_token;
@@ -1992,7 +2160,8 @@ bool use_fused_mlp(int64_t rows, int groups, int64_t max_group_rows, int I) {
 
 cudaError_t gemm_expert_mlp_fused(const bf16* x, int64_t rows, const int32_t* offsets, int E, int H, int I,
                                   const bf16* w_gate_up, const bf16* w_down, bf16* h, bf16* gu_save, bf16* y,
-                                  int32_t* sched, int64_t max_group_rows, cudaStream_t st, unsigned* err) {
+                                  int32_t* sched, int64_t max_group_rows, cudaStream_t st, unsigned* err,
+                                  const Rows8& gu8) {
     if (rows == 0) return cudaSuccess;
     if (!offsets || !sched || max_group_rows <= 0 || max_group_rows > 64 || E > kMaxGroups)
         return cudaErrorInvalidValue;
@@ -2011,6 +2180,8 @@ cudaError_t gemm_expert_mlp_fused(const bf16* x, int64_t rows, const int32_t* of
     p.ldo = I;
     p.out2 = gu_save;
     p.ldo2 = 2 * (int64_t)I;
+    p.gu8 = gu8.q;
+    p.gu8_scale = gu8.scale;
     p.y = y;
     p.ldy = H;
     p.N2 = H;
@@ -2109,6 +2280,35 @@ cudaError_t gemm_down_dgrad_swiglu(const bf16* dy, int64_t rows, const int32_t* 
     CUtensorMap tc;
     if (!make_out_map(&tc, dgu, rows, 2 * (uint64_t)I)) return cudaErrorInvalidValue;
     return launch_group_m<kEpiSwigluBwd, false>(ta, ta64, tb, tb1, p, st, &tc);
+}
+
+cudaError_t gemm_down_dgrad_swiglu8(const bf16* dy, int64_t rows, const int32_t* offsets, int E, int H, int I,
+                                    const bf16* w_down, const Rows8& gu8, const float* row_scale, bf16* dgu, bf16* h,
+                                    float* row_dot, cudaStream_t st, unsigned* err) {
+    if (rows == 0) return cudaSuccess;
+    CUtensorMap ta, ta64, tb, tb1;   // as in gemm_down_dgrad_swiglu
+    if (!make_map_2d(&ta, dy, H, rows, H, BK, 128)) return cudaErrorInvalidValue;
+    if (!make_map_2d(&ta64, dy, H, rows, H, BK, 64)) return cudaErrorInvalidValue;
+    if (!make_map_3d(&tb, w_down, H, I, E, BK, BN / 2)) return cudaErrorInvalidValue;
+    if (!make_map_3d(&tb1, w_down, H, I, E, BK, BN)) return cudaErrorInvalidValue;
+    Params p = base_params(E, rows, offsets, err);
+    p.N = I;
+    p.K = H;
+    p.I = I;
+    p.n_blocks = (I + BN - 1) / BN;
+    p.out = dgu;
+    p.ldo = 2 * (int64_t)I;
+    p.out2 = h;
+    p.ldo2 = I;
+    p.gu8 = gu8.q;
+    p.gu8_scale = gu8.scale;
+    p.row_scale = row_scale;
+    p.row_dot = row_dot;
+    p.ld_row_dot = (I + 63) / 64;
+    CUtensorMap tc, tc2;
+    if (!make_out_map(&tc, dgu, rows, 2 * (uint64_t)I)) return cudaErrorInvalidValue;
+    if (!make_out_map(&tc2, h, rows, I)) return cudaErrorInvalidValue;
+    return launch_group_m<kEpiSwigluBwd8, false>(ta, ta64, tb, tb1, p, st, &tc, &tc2);
 }
 
 cudaError_t gemm_gate_up_dgrad(const bf16* dgu, int64_t rows, const int32_t* offsets, int E, int H,

@@ -147,6 +147,27 @@ BwdLayout bwd_layout(void* ws, int64_t T, int H, int I, int k) {
     return L;
 }
 
+// The backward from the 8-bit state. One [A][H] buffer serves in turn as dy (the
+// rows of dout), dx by row, and x by row: each is dead before the next is written.
+struct Bwd8Layout {
+    bf16 *rows, *dgu, *h;
+    float *prob_row, *row_dot;
+    size_t bytes;
+};
+
+Bwd8Layout bwd8_layout(void* ws, int64_t T, int H, int I, int k) {
+    const int64_t A = T * k;
+    Carver c(ws);
+    Bwd8Layout L;
+    L.rows = c.take<bf16>((size_t)A * H);
+    L.dgu = c.take<bf16>((size_t)A * 2 * I);
+    L.h = c.take<bf16>((size_t)A * I);
+    L.prob_row = c.take<float>((size_t)A);
+    L.row_dot = c.take<float>((size_t)A * ((I + 63) / 64));
+    L.bytes = c.bytes();
+    return L;
+}
+
 struct ScaledBwdLayout {
     bf16 *dy, *dgu, *dx_perm;
     float* row_dot;
@@ -540,14 +561,23 @@ size_t moe_layer_forward_workspace_size(int64_t T, int H, int I, int E, int k, i
     return fwd_layout(nullptr, T, H, I, E, k, has_shared).bytes;
 }
 
-moe_status moe_layer_forward(const float* logits, const moe_bf16* x, int64_t T, int H, int I,
-                             int E, int k, const moe_router_opts* opts_in,
-                             const moe_bf16* w_gate_up, const moe_bf16* w_down,
-                             const moe_bf16* shared_gate_up, const moe_bf16* shared_down,
-                             moe_bf16* out, int32_t* topk_idx, float* topk_prob, int32_t* counts,
-                             int32_t* offsets, int32_t* row_of, moe_bf16* x_perm, moe_bf16* gu,
-                             moe_bf16* h, moe_bf16* y_perm, void* workspace,
-                             size_t workspace_bytes, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// What a layer forward keeps in 8 bits: gu8 from the gate_up epilogue, and x8
+// from the tokens' rows (its pointers NULL when the caller already has it).
+struct Ckpt8 {
+    Rows8 x8, gu8;
+};
+
+// The layer forward of moe_layer_forward and moe_layer_forward_ckpt.
+moe_status layer_forward(const float* logits, const moe_bf16* x, int64_t T, int H, int I, int E, int k,
+                         const moe_router_opts* opts_in, const moe_bf16* w_gate_up, const moe_bf16* w_down,
+                         const moe_bf16* shared_gate_up, const moe_bf16* shared_down, moe_bf16* out,
+                         int32_t* topk_idx, float* topk_prob, int32_t* counts, int32_t* offsets, int32_t* row_of,
+                         moe_bf16* x_perm, moe_bf16* gu, moe_bf16* h, moe_bf16* y_perm, const Ckpt8& keep,
+                         void* workspace, size_t workspace_bytes, void* stream) {
     const ChainScope chain(T * (int64_t)k <= kChainMaxRows);
     if (!shape_ok(T, E, k) || H <= 0 || I <= 0) return MOE_ERR_INVALID_ARG;
     if (!dims_ok(H, I)) return MOE_ERR_UNSUPPORTED;
@@ -601,6 +631,7 @@ moe_status moe_layer_forward(const float* logits, const moe_bf16* x, int64_t T, 
     const int n_zero = fused_mlp ? E + 1 : 0;
 
     cudaError_t e = trace_mark(0, st);
+    if (e == cudaSuccess && keep.x8.q) e = launch_quantize_rows(xb, T, H, 1, 0, keep.x8.q, keep.x8.scale, st);
     bool scanned = false, permuted = false;
     // one token block (T <= 8): the router also writes the counts and offsets
     // (no scan launch), and for at most 64 KB of rows the permuted rows too (no
@@ -618,14 +649,14 @@ moe_status moe_layer_forward(const float* logits, const moe_bf16* x, int64_t T, 
     if (e == cudaSuccess && fused_mlp)
         e = gemm_expert_mlp_fused(L.x_perm, A, L.offsets, E, H, I, reinterpret_cast<const bf16*>(w_gate_up),
                                   reinterpret_cast<const bf16*>(w_down), L.h, reinterpret_cast<bf16*>(gu), L.y_perm,
-                                  L.sched, T, st, err);   // the down stage's trace mark follows at once
+                                  L.sched, T, st, err, keep.gu8);   // the down stage's trace mark follows at once
     else if (e == cudaSuccess)
         e = gather ? gemm_gate_up_swiglu_gather(xb, T, L.sorted_token, A, L.offsets, E, H, I,
                                                 reinterpret_cast<const bf16*>(w_gate_up), L.h,
-                                                reinterpret_cast<bf16*>(gu), st, err)
+                                                reinterpret_cast<bf16*>(gu), st, err, nullptr, keep.gu8)
                    : gemm_gate_up_swiglu(L.x_perm, A, L.offsets, E, H, I,
                                          reinterpret_cast<const bf16*>(w_gate_up), L.h,
-                                         reinterpret_cast<bf16*>(gu), st, err, nullptr, T);
+                                         reinterpret_cast<bf16*>(gu), st, err, nullptr, T, keep.gu8);
     if (e == cudaSuccess) e = trace_mark(3, st);
     if (e == cudaSuccess && !fused_mlp)
         e = gemm_down(L.h, A, L.offsets, E, H, I, reinterpret_cast<const bf16*>(w_down), L.y_perm,
@@ -653,6 +684,44 @@ moe_status moe_layer_forward(const float* logits, const moe_bf16* x, int64_t T, 
                            reinterpret_cast<bf16*>(out), st, err);
     if (e == cudaSuccess) e = trace_mark(6, st);
     return from_cuda(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_layer_forward(const float* logits, const moe_bf16* x, int64_t T, int H, int I,
+                             int E, int k, const moe_router_opts* opts,
+                             const moe_bf16* w_gate_up, const moe_bf16* w_down,
+                             const moe_bf16* shared_gate_up, const moe_bf16* shared_down,
+                             moe_bf16* out, int32_t* topk_idx, float* topk_prob, int32_t* counts,
+                             int32_t* offsets, int32_t* row_of, moe_bf16* x_perm, moe_bf16* gu,
+                             moe_bf16* h, moe_bf16* y_perm, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+    return layer_forward(logits, x, T, H, I, E, k, opts, w_gate_up, w_down, shared_gate_up, shared_down, out,
+                         topk_idx, topk_prob, counts, offsets, row_of, x_perm, gu, h, y_perm, Ckpt8(), workspace,
+                         workspace_bytes, stream);
+}
+
+moe_status moe_layer_forward_ckpt(const float* logits, const moe_bf16* x, int64_t T, int H, int I, int E, int k,
+                                   const moe_router_opts* opts, const moe_bf16* w_gate_up, const moe_bf16* w_down,
+                                   const moe_bf16* shared_gate_up, const moe_bf16* shared_down, moe_bf16* out,
+                                   int32_t* topk_idx, float* topk_prob, int32_t* counts, int32_t* offsets,
+                                   int32_t* row_of, uint8_t* x_q, uint8_t* x_scale, int x_given, uint8_t* gu_q,
+                                   uint8_t* gu_scale, void* workspace, size_t workspace_bytes, void* stream) {
+    if (x_given != 0 && x_given != 1) return MOE_ERR_INVALID_ARG;
+    if (T > 0) {
+        const void* must[] = {topk_idx, topk_prob, offsets, row_of, gu_q, gu_scale};
+        for (const void* p : must)
+            if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+        if (!x_given && (!x_q || !x_scale || !aligned16(x_q) || !aligned16(x_scale))) return MOE_ERR_INVALID_ARG;
+    }
+    Ckpt8 keep;
+    if (!x_given) keep.x8 = Rows8{x_q, x_scale};
+    keep.gu8 = Rows8{gu_q, gu_scale};
+    return layer_forward(logits, x, T, H, I, E, k, opts, w_gate_up, w_down, shared_gate_up, shared_down, out,
+                         topk_idx, topk_prob, counts, offsets, row_of, nullptr, nullptr, nullptr, nullptr, keep,
+                         workspace, workspace_bytes, stream);
 }
 
 size_t moe_grouped_mlp_backward_workspace_size(int64_t T, int H, int I, int E, int k) {
@@ -764,6 +833,134 @@ moe_status moe_grouped_mlp_scaled_backward(const moe_bf16* dout, int64_t T, int 
         e = gemm_wgrad(B(x_perm), L.dgu, A, offsets, E, H, 2 * I, reinterpret_cast<bf16*>(dw_gate_up), st, err);
     if (e == cudaSuccess) e = trace_mark(6, st);
     return from_cuda(e);
+}
+
+size_t moe_grouped_mlp_backward_ckpt_workspace_size(int64_t T, int H, int I, int E, int k) {
+    if (!shape_ok(T, E, k) || !dims_ok(H, I)) return 0;
+    return bwd8_layout(nullptr, T, H, I, k).bytes;
+}
+
+moe_status moe_grouped_mlp_backward_ckpt(const moe_bf16* dout, int64_t T, int H, int I, int E, int k,
+                                          const moe_bf16* w_gate_up, const moe_bf16* w_down, const int32_t* row_of,
+                                          const float* topk_prob, const int32_t* offsets, const uint8_t* x_q,
+                                          const uint8_t* x_scale, const uint8_t* gu_q, const uint8_t* gu_scale,
+                                          moe_bf16* dx, moe_bf16* dw_gate_up, moe_bf16* dw_down, float* dprob,
+                                          void* workspace, size_t workspace_bytes, void* stream) {
+    const ChainScope chain(T * (int64_t)k <= kChainMaxRows);
+    if (!shape_ok(T, E, k) || H <= 0 || I <= 0) return MOE_ERR_INVALID_ARG;
+    if (!dims_ok(H, I)) return MOE_ERR_UNSUPPORTED;
+    if (!dw_gate_up || !dw_down || !aligned16(dw_gate_up) || !aligned16(dw_down)) return MOE_ERR_INVALID_ARG;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {   // no rows: only the weight gradients have elements, and they are zero
+        const size_t n = (size_t)E * (size_t)H * (size_t)I * sizeof(bf16);
+        if (cudaMemsetAsync(dw_gate_up, 0, 2 * n, st) != cudaSuccess) return MOE_ERR_CUDA;
+        return from_cuda(cudaMemsetAsync(dw_down, 0, n, st));
+    }
+    const void* must[] = {dout, w_gate_up, w_down, row_of, topk_prob, offsets, x_q, x_scale, gu_q, gu_scale, dx,
+                          dprob};
+    for (const void* p : must)
+        if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < bwd8_layout(nullptr, T, H, I, k).bytes)
+        return MOE_ERR_WORKSPACE;
+    unsigned* err = device_error_word();
+    if (!err) return MOE_ERR_CUDA;
+    const Bwd8Layout L = bwd8_layout(workspace, T, H, I, k);
+    const int64_t A = T * k;
+    auto B = [](const moe_bf16* p) { return reinterpret_cast<const bf16*>(p); };
+    const Rows8 gu8{const_cast<uint8_t*>(gu_q), const_cast<uint8_t*>(gu_scale)};   // read only
+    cudaError_t e = trace_mark(0, st);
+    if (e == cudaSuccess)
+        e = launch_spread_rows(B(dout), row_of, topk_prob, T, k, H, A, L.rows, L.prob_row, st, err);
+    if (e == cudaSuccess) e = trace_mark(1, st);
+    if (e == cudaSuccess)
+        e = gemm_down_dgrad_swiglu8(L.rows, A, offsets, E, H, I, B(w_down), gu8, L.prob_row, L.dgu, L.h, L.row_dot,
+                                    st, err);
+    if (e == cudaSuccess) e = launch_row_dot_sum(L.row_dot, (I + 63) / 64, row_of, A, A, dprob, st, err);
+    if (e == cudaSuccess) e = trace_mark(2, st);
+    if (e == cudaSuccess)
+        e = gemm_wgrad(L.h, L.rows, A, offsets, E, I, H, reinterpret_cast<bf16*>(dw_down), st, err);
+    if (e == cudaSuccess) e = trace_mark(3, st);
+    // dy is done with: its buffer takes each row's dx, and then each row's x
+    if (e == cudaSuccess)
+        e = gemm_gate_up_dgrad(L.dgu, A, offsets, E, H, I, B(w_gate_up), L.rows, st, err);
+    if (e == cudaSuccess) e = trace_mark(4, st);
+    if (e == cudaSuccess)
+        e = launch_combine(L.rows, row_of, nullptr, T, k, H, A, nullptr, reinterpret_cast<bf16*>(dx), st, err);
+    if (e == cudaSuccess) e = trace_mark(5, st);
+    if (e == cudaSuccess) e = launch_spread_rows8(x_q, x_scale, row_of, T, k, H, A, L.rows, st, err);
+    if (e == cudaSuccess)
+        e = gemm_wgrad(L.rows, L.dgu, A, offsets, E, H, 2 * I, reinterpret_cast<bf16*>(dw_gate_up), st, err);
+    if (e == cudaSuccess) e = trace_mark(6, st);
+    return from_cuda(e);
+}
+
+namespace {
+// Rows of the 8-bit format: columns in eights, one or two parts, the last row's
+// end and the scales within what an offset holds.
+bool rows8_ok(int64_t rows, int cols, int parts, int block_major) {
+    return rows >= 0 && rows < (int64_t(1) << 31) && cols > 0 && cols % 8 == 0 && cols <= (1 << 24) &&
+           (parts == 1 || parts == 2) && (block_major == 0 || block_major == 1);
+}
+}  // namespace
+
+moe_status moe_quantize_rows(const moe_bf16* x, int64_t rows, int cols, int parts, int block_major, uint8_t* q,
+                             uint8_t* scale, void* stream) {
+    if (!rows8_ok(rows, cols, parts, block_major)) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!x || !q || !scale || !aligned16(x) || !aligned16(q) || !aligned16(scale)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(launch_quantize_rows(reinterpret_cast<const bf16*>(x), rows, cols, parts, block_major, q, scale,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_dequantize_rows(const uint8_t* q, const uint8_t* scale, int64_t rows, int cols, int parts,
+                               int block_major, moe_bf16* x, void* stream) {
+    if (!rows8_ok(rows, cols, parts, block_major)) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (!x || !q || !scale || !aligned16(x) || !aligned16(q) || !aligned16(scale)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(launch_dequantize_rows(q, scale, rows, cols, parts, block_major, reinterpret_cast<bf16*>(x),
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_rmsnorm(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* weight, int64_t T, int H,
+                       float eps, moe_bf16* sum, moe_bf16* y, uint8_t* y_q, uint8_t* y_scale, float* rstd,
+                       void* stream) {
+    if (T < 0 || T >= (int64_t(1) << 31) || H <= 0 || !(eps >= 0.0f) || eps > 3.0e38f) return MOE_ERR_INVALID_ARG;
+    if (H % 8 != 0 || H > kRmsnormMaxH) return MOE_ERR_UNSUPPORTED;
+    if ((y_q == nullptr) != (y_scale == nullptr) || (sum != nullptr && residual == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!x || !weight || (!y && !y_q)) return MOE_ERR_INVALID_ARG;
+    const void* all[] = {x, residual, weight, sum, y, y_q, y_scale, rstd};
+    for (const void* p : all)
+        if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
+    auto B = [](const moe_bf16* p) { return reinterpret_cast<const bf16*>(p); };
+    return from_cuda(launch_rmsnorm(B(x), B(residual), B(weight), T, H, eps, reinterpret_cast<bf16*>(sum),
+                                    reinterpret_cast<bf16*>(y), y_q, y_scale, rstd,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_rmsnorm_backward_workspace_size(int64_t T, int H) {
+    if (T < 0 || T >= (int64_t(1) << 31) || H <= 0 || H % 8 != 0 || H > kRmsnormMaxH) return 0;
+    return rmsnorm_backward_workspace_bytes(T, H);
+}
+
+moe_status moe_rmsnorm_backward(const moe_bf16* dy, const moe_bf16* s, const moe_bf16* weight, const float* rstd,
+                                const moe_bf16* dsum, int64_t T, int H, moe_bf16* dx, float* dweight,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    if (T < 0 || T >= (int64_t(1) << 31) || H <= 0) return MOE_ERR_INVALID_ARG;
+    if (H % 8 != 0 || H > kRmsnormMaxH) return MOE_ERR_UNSUPPORTED;
+    if (dweight && !aligned16(dweight)) return MOE_ERR_INVALID_ARG;
+    if (T > 0) {
+        const void* must[] = {dy, s, weight, rstd, dx};
+        for (const void* p : must)
+            if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+        if (dsum && !aligned16(dsum)) return MOE_ERR_INVALID_ARG;
+        if (dweight && (!workspace || !aligned16(workspace) || workspace_bytes < rmsnorm_backward_workspace_bytes(T, H)))
+            return MOE_ERR_WORKSPACE;
+    }
+    auto B = [](const moe_bf16* p) { return reinterpret_cast<const bf16*>(p); };
+    return from_cuda(launch_rmsnorm_backward(B(dy), B(s), B(weight), rstd, B(dsum), T, H,
+                                             reinterpret_cast<bf16*>(dx), dweight, static_cast<float*>(workspace),
+                                             static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -135,10 +135,39 @@ cudaError_t launch_gather_rows(const bf16* dout, const int32_t* sorted_token, in
 cudaError_t launch_row_dot_sum(const float* row_dot, int nq, const int32_t* row_of, int64_t n, int64_t A,
                                float* dprob, cudaStream_t st, unsigned* err);
 
+// Values in the 8-bit row format and their scale bytes (rows8.cuh, rows8.cu).
+// Rows of parts * cols columns (parts 1 or 2, each with its own blocks); scales
+// [rows][parts * S], or [parts * S][rows] when block_major, S = ceil(cols / 32).
+struct Rows8 {
+    uint8_t* q = nullptr;
+    uint8_t* scale = nullptr;
+};
+cudaError_t launch_quantize_rows(const bf16* x, int64_t rows, int cols, int parts, int block_major, uint8_t* q,
+                                 uint8_t* scale, cudaStream_t st);
+cudaError_t launch_dequantize_rows(const uint8_t* q, const uint8_t* scale, int64_t rows, int cols, int parts,
+                                   int block_major, bf16* x, cudaStream_t st);
+// rows[row_of[t, j]] = src[t] for every assignment (and prob_row[row] = prob[t, j]
+// when prob_row is given); launch_spread_rows8 reads src from 8 bits.
+cudaError_t launch_spread_rows(const bf16* src, const int32_t* row_of, const float* prob, int64_t T, int k, int H,
+                               int64_t A, bf16* rows, float* prob_row, cudaStream_t st, unsigned* err);
+cudaError_t launch_spread_rows8(const uint8_t* q, const uint8_t* scale, const int32_t* row_of, int64_t T, int k,
+                                int H, int64_t A, bf16* rows, cudaStream_t st, unsigned* err);
+
+// RMSNorm with the residual's addition, and its backward (rmsnorm.cu).
+constexpr int kRmsnormMaxH = 16384;
+cudaError_t launch_rmsnorm(const bf16* x, const bf16* residual, const bf16* weight, int64_t T, int H, float eps,
+                           bf16* sum, bf16* y, uint8_t* y_q, uint8_t* y_scale, float* rstd, cudaStream_t st);
+size_t rmsnorm_backward_workspace_bytes(int64_t T, int H);
+cudaError_t launch_rmsnorm_backward(const bf16* dy, const bf16* s, const bf16* weight, const float* rstd,
+                                    const bf16* dsum, int64_t T, int H, bf16* dx, float* dweight, float* partial,
+                                    cudaStream_t st);
+
 // ---------------------------------------------------------------- GEMMs
 // Grouped GEMMs on tcgen05. Each returns cudaErrorInvalidValue if a tensor
 // map cannot be encoded (bad alignment or extent).
-// gate_up + SwiGLU: h[r] = silu(x[r] Wg[e]) * (x[r] Wu[e]); optionally gu[r] = [g | u].
+// gate_up + SwiGLU: h[r] = silu(x[r] Wg[e]) * (x[r] Wu[e]); optionally gu[r] = [g | u]
+// in bf16 (gu_save) and, from the fp32 accumulators, in 8 bits (gu8: two parts of I
+// columns, block-major scales).
 // offsets NULL: one group of `rows` rows using the weights of group 0.
 // max_group_rows: an upper bound on the rows of any group (0: rows), which
 // lets small batches take narrower swap-AB tiles (a layer call passes T: a
@@ -146,14 +175,14 @@ cudaError_t launch_row_dot_sum(const float* row_dot, int nq, const int32_t* row_
 cudaError_t gemm_gate_up_swiglu(const bf16* x, int64_t rows, const int32_t* offsets, int E, int H,
                                 int I, const bf16* w_gate_up, bf16* h, bf16* gu_save,
                                 cudaStream_t st, unsigned* err, const float* row_scale = nullptr,
-                                int64_t max_group_rows = 0);
+                                int64_t max_group_rows = 0, const Rows8& gu8 = Rows8());
 // gate_up + SwiGLU with A row r gathered from x: row sorted_token[r] (-1: a
 // zero row) of x [T][H], so no permuted copy of x is needed. Single-CTA tiles
 // only; H a multiple of 8 and x 16-byte aligned.
 cudaError_t gemm_gate_up_swiglu_gather(const bf16* x, int64_t T, const int32_t* sorted_token, int64_t rows,
                                        const int32_t* offsets, int E, int H, int I, const bf16* w_gate_up, bf16* h,
                                        bf16* gu_save, cudaStream_t st, unsigned* err,
-                                       const float* row_scale = nullptr);
+                                       const float* row_scale = nullptr, const Rows8& gu8 = Rows8());
 // The expert MLP of a small batch in one launch (gemm_swap_mlp_kernel):
 // h = SwiGLU(x W_gate_up) (and gu = [g | u] if gu_save), then y = h W_down,
 // on swap-AB tiles. Every expert must hold at most max_group_rows <= 64 rows
@@ -163,7 +192,8 @@ cudaError_t gemm_gate_up_swiglu_gather(const bf16* x, int64_t T, const int32_t* 
 bool use_fused_mlp(int64_t rows, int groups, int64_t max_group_rows, int I);
 cudaError_t gemm_expert_mlp_fused(const bf16* x, int64_t rows, const int32_t* offsets, int E, int H, int I,
                                   const bf16* w_gate_up, const bf16* w_down, bf16* h, bf16* gu_save, bf16* y,
-                                  int32_t* sched, int64_t max_group_rows, cudaStream_t st, unsigned* err);
+                                  int32_t* sched, int64_t max_group_rows, cudaStream_t st, unsigned* err,
+                                  const Rows8& gu8 = Rows8());
 // Whether the forward gate_up GEMM runs on single-CTA 128-row tiles (not CTA
 // pairs, not swap-AB tiles) for this many rows and groups.
 bool grouped_gemm_single_tiles(int64_t rows, int groups);
@@ -188,6 +218,12 @@ cudaError_t gemm_down_dgrad_swiglu(const bf16* dy, int64_t rows, const int32_t* 
                                    int H, int I, const bf16* w_down, const bf16* gu, bf16* dgu,
                                    cudaStream_t st, unsigned* err, const float* row_scale = nullptr,
                                    float* row_dot = nullptr);
+// dgrad of down with the SwiGLU backward from an 8-bit [g | u] (gu8 as above): as
+// gemm_down_dgrad_swiglu with row_scale and row_dot, and h[r] = row_scale[r] *
+// silu(g) * u, recomputed, for the down weight's gradient.
+cudaError_t gemm_down_dgrad_swiglu8(const bf16* dy, int64_t rows, const int32_t* offsets, int E, int H, int I,
+                                    const bf16* w_down, const Rows8& gu8, const float* row_scale, bf16* dgu, bf16* h,
+                                    float* row_dot, cudaStream_t st, unsigned* err);
 // dgrad of gate_up: dx_perm = dgu Wgu[e]^T
 cudaError_t gemm_gate_up_dgrad(const bf16* dgu, int64_t rows, const int32_t* offsets, int E, int H,
                                int I, const bf16* w_gate_up, bf16* dx_perm, cudaStream_t st,
