@@ -18,6 +18,7 @@ layer's x in that format as well.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -176,23 +177,29 @@ def _need(t: torch.Tensor, dtype, name: str) -> None:
 
 def _need_shape(t: torch.Tensor, dtype, shape: tuple, name: str) -> None:
     _need(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _on_device(tensors):
-    """The CUDA device that all given tensors (None is skipped) are on, as a
-    context in which it is the current one, so that the call takes that device's
-    current stream and its kernels run there."""
-    device = None
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on_device(*tensors):
+    """(context, stream): the CUDA device that all given tensors (None is skipped)
+    are on, as a context in which it is the current one, and its current stream.
+    By torch's raw getters: the public current_stream() and a context that changes
+    nothing take about as long as the launch itself (3.2 + 1.5 us, against 4)."""
+    index = -1
     for t in tensors:
         if t is None:
             continue
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"tensors on different devices: {device} and {t.device}")
-    return torch.cuda.device(device)
+        i = t.get_device()
+        if index < 0:
+            index = i
+        elif i != index:
+            raise ValueError(f"tensors on different devices: cuda:{index} and cuda:{i}")
+    context = _HERE_ALREADY if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
+    return context, torch._C._cuda_getCurrentRawStream(index)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -652,11 +659,12 @@ def moe_quantize_rows(x: torch.Tensor, parts: int = 1, block_major: bool = False
     [blocks, rows]."""
     _need(x, torch.bfloat16, "x")
     rows, cols, scale_shape = _rows8_shape(x, parts, block_major)
-    with _on_device([x]):
-        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-        scale = torch.empty(scale_shape, dtype=torch.uint8, device=x.device)
-        _check(lib().moe_quantize_rows(_ptr(x), rows, cols, parts, int(block_major), _ptr(q), _ptr(scale), _stream()),
-               "moe_quantize_rows")
+    context, stream = _on_device(x)
+    with context:
+        q = torch.empty_like(x, dtype=torch.uint8)
+        scale = x.new_empty(scale_shape, dtype=torch.uint8)
+        _check(lib().moe_quantize_rows(x.data_ptr(), rows, cols, parts, block_major, q.data_ptr(), scale.data_ptr(),
+                                       stream), "moe_quantize_rows")
     return q, scale
 
 
@@ -670,11 +678,12 @@ def moe_dequantize_rows(q: torch.Tensor, scale: torch.Tensor, parts: int = 1, bl
     _need_shape(scale, torch.uint8, scale_shape, "scale")
     if out is not None:
         _need_shape(out, torch.bfloat16, q.shape, "out")
-    with _on_device([q, scale, out]):
+    context, stream = _on_device(q, scale, out)
+    with context:
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        _check(lib().moe_dequantize_rows(_ptr(q), _ptr(scale), rows, cols, parts, int(block_major), _ptr(out),
-                                         _stream()), "moe_dequantize_rows")
+            out = torch.empty_like(q, dtype=torch.bfloat16)
+        _check(lib().moe_dequantize_rows(q.data_ptr(), scale.data_ptr(), rows, cols, parts, block_major,
+                                         out.data_ptr(), stream), "moe_dequantize_rows")
     return out
 
 
@@ -700,22 +709,22 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Opt
     if quantize:
         want["y_q"] = (torch.uint8, (T, H))
         want["y_scale"] = (torch.uint8, (T, -(-H // ROWS8_BLOCK)))
-    given = dict(out or {})
-    for name in given:
+    r = dict(out) if out else {}
+    for name, t in r.items():
         if name not in want:
             raise ValueError(f"out: this call does not write {name!r}")
-    with _on_device([x, weight, residual, *given.values()]):
-        r = {}
+        if t is not None:
+            _need_shape(t, *want[name], name)
+    context, stream = _on_device(x, weight, residual, *r.values())
+    with context:
         for name, (dtype, shape) in want.items():
-            if name not in given:
-                r[name] = torch.empty(shape, dtype=dtype, device=x.device)
-            else:
-                r[name] = given[name]
-                if r[name] is not None:
-                    _need_shape(r[name], dtype, shape, name)
+            if name not in r:
+                r[name] = torch.empty_like(x, dtype=dtype) if len(shape) == 2 and shape[1] == H else x.new_empty(
+                    shape, dtype=dtype)
         g = r.get
-        _check(lib().moe_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), T, H, float(eps), _ptr(g("sum")), _ptr(g("y")),
-                                 _ptr(g("y_q")), _ptr(g("y_scale")), _ptr(g("rstd")), _stream()), "moe_rmsnorm")
+        _check(lib().moe_rmsnorm(x.data_ptr(), _ptr(residual), weight.data_ptr(), T, H, eps, _ptr(g("sum")),
+                                 _ptr(r["y"]), _ptr(g("y_q")), _ptr(g("y_scale")), _ptr(r["rstd"]), stream),
+               "moe_rmsnorm")
     if residual is None:
         r["sum"] = x
     return r
@@ -739,15 +748,16 @@ def moe_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor
             _need_shape(t, torch.bfloat16, (T, H), n)
     if workspace is not None:
         _need(workspace, torch.uint8, "workspace")
-    with _on_device([dy, s, weight, rstd, dsum, dx, workspace]):
+    context, stream = _on_device(dy, s, weight, rstd, dsum, dx, workspace)
+    with context:
         if dx is None:
-            dx = torch.empty((T, H), dtype=torch.bfloat16, device=dy.device)
-        dweight = torch.empty(H, dtype=torch.float32, device=dy.device) if want_dweight else None
+            dx = torch.empty_like(dy)
+        dweight = rstd.new_empty((H,)) if want_dweight else None
         if workspace is None and want_dweight:
             workspace = _workspace(lib().moe_rmsnorm_backward_workspace_size(T, H), dy.device)
-        _check(lib().moe_rmsnorm_backward(_ptr(dy), _ptr(s), _ptr(weight), _ptr(rstd), _ptr(dsum), T, H, _ptr(dx),
-                                          _ptr(dweight), _ptr(workspace),
-                                          0 if workspace is None else workspace.numel(), _stream()),
+        _check(lib().moe_rmsnorm_backward(dy.data_ptr(), s.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _ptr(dsum),
+                                          T, H, dx.data_ptr(), _ptr(dweight), _ptr(workspace),
+                                          0 if workspace is None else workspace.numel(), stream),
                "moe_rmsnorm_backward")
     return {"dx": dx, "dweight": dweight}
 
@@ -816,13 +826,14 @@ def moe_layer_forward_ckpt(logits: torch.Tensor, x: torch.Tensor, w_gate_up: tor
             _need_shape(t, spec[name][0], spec[name][1], name)
     if out is not None:
         _need_shape(out, torch.bfloat16, (T, H), "out")
-    with _on_device([logits, x, w_gate_up, w_down, shared_gate_up, shared_down, out, opts.expert_bias,
-                     *[st[n] for n in spec if n in st], None if workspace is None else workspace.fwd]):
+    context, stream = _on_device(logits, x, w_gate_up, w_down, shared_gate_up, shared_down, out, opts.expert_bias,
+                                 *[st[n] for n in spec if n in st], None if workspace is None else workspace.fwd)
+    with context:
         if out is None:
-            out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+            out = torch.empty_like(x)
         for name, (dtype, shape) in spec.items():
             if name not in st:
-                st[name] = torch.empty(shape, dtype=dtype, device=x.device)
+                st[name] = x.new_empty(shape, dtype=dtype)
         if workspace is None:
             workspace = LayerWorkspace(T, H, I, E, k, shared_gate_up is not None, device=x.device)
         oc = opts.c()
@@ -831,7 +842,7 @@ def moe_layer_forward_ckpt(logits: torch.Tensor, x: torch.Tensor, w_gate_up: tor
             _ptr(shared_gate_up), _ptr(shared_down), _ptr(out), _ptr(st["topk_idx"]), _ptr(st["topk_prob"]),
             _ptr(st["counts"]), _ptr(st["offsets"]), _ptr(st["row_of"]), _ptr(st["x_q"]), _ptr(st["x_scale"]),
             int(x8 is not None), _ptr(st["gu_q"]), _ptr(st["gu_scale"]), _ptr(workspace.fwd), workspace.fwd.numel(),
-            _stream()), "moe_layer_forward_ckpt")
+            stream), "moe_layer_forward_ckpt")
     return out, st
 
 
@@ -859,15 +870,16 @@ def moe_grouped_mlp_backward_ckpt(dout: torch.Tensor, state: dict, w_gate_up: to
         if name in g:
             _need_shape(g[name], dtype, shape, name)
     ws = None if workspace is None else workspace.bwd8
-    with _on_device([dout, w_gate_up, w_down, ws, *[s[n] for n in used], *[g[n] for n in want if n in g]]):
+    context, stream = _on_device(dout, w_gate_up, w_down, ws, *[s[n] for n in used], *[g[n] for n in want if n in g])
+    with context:
         for name, (dtype, shape) in want.items():
             if name not in g:
-                g[name] = torch.empty(shape, dtype=dtype, device=dout.device)
+                g[name] = dout.new_empty(shape, dtype=dtype)
         if ws is None:
             ws = _workspace(lib().moe_grouped_mlp_backward_ckpt_workspace_size(T, H, I, E, k), dout.device)
         _check(lib().moe_grouped_mlp_backward_ckpt(
             _ptr(dout), T, H, I, E, k, _ptr(w_gate_up), _ptr(w_down), _ptr(s["row_of"]), _ptr(s["topk_prob"]),
             _ptr(s["offsets"]), _ptr(s["x_q"]), _ptr(s["x_scale"]), _ptr(s["gu_q"]), _ptr(s["gu_scale"]),
             _ptr(g["dx"]), _ptr(g["dw_gate_up"]), _ptr(g["dw_down"]), _ptr(g["dprob"]), _ptr(ws), ws.numel(),
-            _stream()), "moe_grouped_mlp_backward_ckpt")
+            stream), "moe_grouped_mlp_backward_ckpt")
     return g

@@ -957,10 +957,12 @@ moe_status moe_rmsnorm_backward(const moe_bf16* dy, const moe_bf16* s, const moe
         if (dweight && (!workspace || !aligned16(workspace) || workspace_bytes < rmsnorm_backward_workspace_bytes(T, H)))
             return MOE_ERR_WORKSPACE;
     }
+    unsigned* err = T > 0 ? device_error_word() : nullptr;
+    if (T > 0 && !err) return MOE_ERR_CUDA;
     auto B = [](const moe_bf16* p) { return reinterpret_cast<const bf16*>(p); };
     return from_cuda(launch_rmsnorm_backward(B(dy), B(s), B(weight), rstd, B(dsum), T, H,
                                              reinterpret_cast<bf16*>(dx), dweight, static_cast<float*>(workspace),
-                                             static_cast<cudaStream_t>(stream)));
+                                             static_cast<cudaStream_t>(stream), err));
 }
 
 }  // extern "C"

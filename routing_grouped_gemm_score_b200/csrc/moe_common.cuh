@@ -147,6 +147,15 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
         : "memory");
 }
 
+// Bulk copy of `bytes` consecutive bytes into shared memory, completing on an
+// mbarrier. Both addresses and the size are multiples of 16.
+__device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 // L2 policy for loads that later tiles read again (activation panels):
 // evict them after lines without this policy.
 __device__ __forceinline__ uint64_t l2_policy_evict_last() {

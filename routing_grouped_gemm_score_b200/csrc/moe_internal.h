@@ -160,7 +160,7 @@ cudaError_t launch_rmsnorm(const bf16* x, const bf16* residual, const bf16* weig
 size_t rmsnorm_backward_workspace_bytes(int64_t T, int H);
 cudaError_t launch_rmsnorm_backward(const bf16* dy, const bf16* s, const bf16* weight, const float* rstd,
                                     const bf16* dsum, int64_t T, int H, bf16* dx, float* dweight, float* partial,
-                                    cudaStream_t st);
+                                    cudaStream_t st, unsigned* err);
 
 // ---------------------------------------------------------------- GEMMs
 // Grouped GEMMs on tcgen05. Each returns cudaErrorInvalidValue if a tensor

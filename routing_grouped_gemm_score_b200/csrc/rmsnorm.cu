@@ -20,7 +20,12 @@ namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kMaxWarps = 16;      // of a block that owns one row
-constexpr int kWarpRows = 4;       // rows of a block whose warps own one row each
+constexpr size_t kBwdSmem = 200 * 1024;   // an SM's shared memory for the backward's rings
+// Backward threads an SM: 1024 and 1536 measured alike at 5120 columns (59 us for
+// 8192 rows), and at 2048 (4096 rows) 14.2 + 3.5 against 13.8 + 4.5 us, since more
+// blocks leave more partial sums; 512 takes 17.4 and 98 us.
+constexpr int kBwdThreads = 1024;
+constexpr int kMaxStages = 8;      // row slots of a backward block's ring
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -43,21 +48,19 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// One row per block (WARP false; blockDim.x threads hold CH 8-column chunks
-// each) or per warp (WARP true). The pointers may alias as documented (sum with
+// Forward. One row per block, whose threads hold CH 8-column chunks each. The
+// pointers may alias as documented (sum with
 // x or residual): a row's elements are read before they are written, by the
 // same thread, so no pointer is marked restrict or read through the
 // non-coherent path.
-template <int CH, bool WARP>
+template <int CH>
 __global__ void __launch_bounds__(32 * kMaxWarps)
-    rmsnorm_kernel(const uint4* x, const uint4* residual, const uint4* weight, int64_t T, int H, float eps,
+    rmsnorm_kernel(const uint4* x, const uint4* residual, const uint4* weight, int H, float eps,
                                uint4* sum, uint4* y, uint8_t* y_q, uint8_t* y_scale, float* rstd_out) {
     __shared__ float red[kMaxWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int width = WARP ? 32 : (int)blockDim.x;
-    const int me = WARP ? lane : (int)threadIdx.x;
-    const int64_t t = WARP ? (int64_t)blockIdx.x * kWarpRows + warp : (int64_t)blockIdx.x;
-    if (t >= T) return;   // WARP: whole warps
+    const int width = (int)blockDim.x, me = (int)threadIdx.x;
+    const int64_t t = blockIdx.x;
     const int chunks = H / 8;
     uint4 xv[CH], rv[CH], wv[CH];
 #pragma unroll
@@ -88,12 +91,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
         for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
     }
     ss = warp_sum(ss);
-    if (!WARP) {
-        if (lane == 0) red[warp] = ss;
-        __syncthreads();
-        ss = 0.0f;
-        for (int i = 0; i < (int)(blockDim.x >> 5); ++i) ss += red[i];
-    }
+    if (lane == 0) red[warp] = ss;
+    __syncthreads();
+    ss = 0.0f;
+    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) ss += red[i];
     const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
     if (rstd_out && me == 0) rstd_out[t] = rstd;
     const int S = rows8_blocks(H);
@@ -120,24 +121,56 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
     }
 }
 
+// Rows that a block of the backward reduces together: their sums share one
+// barrier, which pays where a row is short.
 template <int CH>
 struct BwdRows {
-    static constexpr int value = CH == 1 ? 4 : CH == 2 ? 2 : 1;   // rows of one block step
+    static constexpr int value = CH == 1 ? 2 : 1;
 };
 
-// A block owns whole rows, R of them a step (one barrier for R sums), and keeps
-// its threads' columns of dweight in registers over all of its rows; partial
-// [gridDim.x][H] gets them at the end. dx may be dy or dsum itself.
+// Backward. A block owns groups of R whole rows (blockIdx.x, + gridDim.x, ...)
+// and keeps its threads' columns of dweight in registers over all of them;
+// partial [gridDim.x][H] gets them at the end. The rows of dy, s and dsum come as
+// bulk asynchronous copies into a ring of `stages` slots in shared memory, one
+// group each, so that loads are in flight while a group is reduced and written,
+// whatever the block's registers hold. A group's slot is read twice, before and
+// after the barrier of its reduction; the next group's barrier says that every
+// thread is done with it, and it is filled again. dx may be dy or dsum itself: a
+// row is written after its own copy has landed, by the block that alone reads it.
+// Every wait is bounded; on a timeout the block records it and leaves.
 template <int CH>
 __global__ void __launch_bounds__(32 * kMaxWarps)
-    rmsnorm_backward_kernel(const uint4* dy, const uint4* s, const uint4* __restrict__ weight,
-                                        const float* __restrict__ rstd, const uint4* dsum, int64_t T, int H,
-                                        uint4* dx, float* __restrict__ partial) {
+    rmsnorm_backward_kernel(const bf16* dy, const bf16* s, const uint4* __restrict__ weight,
+                            const float* __restrict__ rstd, const bf16* dsum, int64_t T, int H, uint4* dx,
+                            float* __restrict__ partial, int stages, unsigned* err) {
     constexpr int R = BwdRows<CH>::value;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ uint64_t full[kMaxStages];
     __shared__ float red[2][R][kMaxWarps];
+    __shared__ int gave_up;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int width = blockDim.x, chunks = H / 8;
     const float inv_h = 1.0f / (float)H;
+    const uint32_t row_bytes = 2u * (uint32_t)H, slot_bytes = (dsum ? 3u : 2u) * R * row_bytes;
+    const int64_t groups = (T + R - 1) / R;
+    int fills = 0;   // thread 0: slots filled so far; fill j used slot j % stages
+    auto fill = [&](int64_t group, int slot) {
+        ++fills;
+        uint8_t* to = ring + slot * slot_bytes;
+        const int64_t at = group * R * H;
+        const uint32_t bytes = row_bytes * (uint32_t)min((int64_t)R, T - group * R);
+        mbar_arrive_expect_tx(&full[slot], (dsum ? 3u : 2u) * bytes);
+        bulk_load(&full[slot], to, dy + at, bytes);
+        bulk_load(&full[slot], to + R * row_bytes, s + at, bytes);
+        if (dsum) bulk_load(&full[slot], to + 2 * R * row_bytes, dsum + at, bytes);
+    };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+        gave_up = 0;
+        fence_mbar_init();
+        fence_proxy_async_smem();
+        for (int64_t g = blockIdx.x; g < groups && fills < stages; g += gridDim.x) fill(g, fills);   // every slot
+    }
     uint4 wv[CH];
     float dw[CH][8];
 #pragma unroll
@@ -147,66 +180,96 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
     }
-    int turn = 0;
-    for (int64_t t0 = (int64_t)blockIdx.x * R; t0 < T; t0 += (int64_t)gridDim.x * R, turn ^= 1) {
-        uint4 g[R][CH], v[R][CH], d[R][CH];
-        float rs[R];
+    float rs_next[R];
+    auto load_rstd = [&](int64_t group) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) rs_next[r] = group * R + r < T ? rstd[group * R + r] : 0.0f;
+    };
+    load_rstd(blockIdx.x);
+    __syncthreads();   // the barriers are initialised
+    int slot = 0, prev = 0, turn = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
+        float rs[R], dot[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int64_t t = t0 + r;
-            rs[r] = t < T ? rstd[t] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int c = threadIdx.x + i * width;
-                g[r][i] = v[r][i] = d[r][i] = make_uint4(0, 0, 0, 0);
-                if (t >= T || c >= chunks) continue;
-                g[r][i] = dy[t * chunks + c];
-                v[r][i] = s[t * chunks + c];
-                if (dsum) d[r][i] = dsum[t * chunks + c];
-            }
+            rs[r] = rs_next[r];
+            dot[r] = 0.0f;
         }
+        load_rstd(g + gridDim.x);
+        ok = mbar_wait(&full[slot], phase, &gave_up, err);
+        const int rows = (int)min((int64_t)R, T - g * R);
+        const uint4* g_rows = reinterpret_cast<const uint4*>(ring + slot * slot_bytes);
+        const uint4* s_rows = g_rows + R * chunks;
+        if (ok) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float dot = 0.0f;
+            for (int r = 0; r < R; ++r) {
+                if (r >= rows) break;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                float gf[8], vf[8], wf[8];
-                unpack8(g[r][i], gf);
-                unpack8(v[r][i], vf);
-                unpack8(wv[i], wf);
+                for (int i = 0; i < CH; ++i) {
+                    const int c = threadIdx.x + i * width;
+                    if (c >= chunks) continue;
+                    float gf[8], vf[8], wf[8];
+                    unpack8(g_rows[r * chunks + c], gf);
+                    unpack8(s_rows[r * chunks + c], vf);
+                    unpack8(wv[i], wf);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float xhat = vf[j] * rs[r];
-                    dw[i][j] += gf[j] * xhat;
-                    dot += gf[j] * wf[j] * xhat;
+                    for (int j = 0; j < 8; ++j) {
+                        const float xhat = vf[j] * rs[r];
+                        dw[i][j] += gf[j] * xhat;
+                        dot[r] += gf[j] * wf[j] * xhat;
+                    }
                 }
             }
-            dot = warp_sum(dot);
-            if (lane == 0) red[turn][r][warp] = dot;
         }
-        __syncthreads();   // red[turn] is written again two steps on, after the next step's barrier
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int64_t t = t0 + r;
+            dot[r] = warp_sum(dot[r]);
+            if (lane == 0) red[turn][r][warp] = dot[r];   // read until the next barrier, written again after it
+        }
+        if (__syncthreads_or(!ok)) break;   // after a timeout every thread leaves
+        if (threadIdx.x == 0 && g != blockIdx.x) {   // the group before is done with: its slot takes the next one to come
+            const int64_t next = g + (int64_t)(stages - 1) * gridDim.x;
+            if (next < groups) fill(next, prev);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (r >= rows) break;
             float c0 = 0.0f;
             for (int w = 0; w < warps; ++w) c0 += red[turn][r][w];
             c0 *= inv_h;
-            if (t >= T) continue;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 const int c = threadIdx.x + i * width;
                 if (c >= chunks) continue;
-                float gf[8], vf[8], wf[8], df[8], o[8];
-                unpack8(g[r][i], gf);
-                unpack8(v[r][i], vf);
+                float gf[8], vf[8], wf[8], o[8];
+                unpack8(g_rows[r * chunks + c], gf);
+                unpack8(s_rows[r * chunks + c], vf);
                 unpack8(wv[i], wf);
-                unpack8(d[r][i], df);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = rs[r] * (gf[j] * wf[j] - vf[j] * rs[r] * c0) + df[j];
-                dx[t * chunks + c] = pack8(o);
+                for (int j = 0; j < 8; ++j) o[j] = rs[r] * (gf[j] * wf[j] - vf[j] * rs[r] * c0);
+                if (dsum) {
+                    float df[8];
+                    unpack8(s_rows[(R + r) * chunks + c], df);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[j] += df[j];
+                }
+                dx[(g * R + r) * chunks + c] = pack8(o);
             }
         }
+        turn ^= 1;
+        prev = slot;
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1u;
+        }
     }
+    if (!ok && threadIdx.x == 0) {   // copies still in flight land before the block's shared memory is given up
+        for (int i = 0; i < stages; ++i)
+            if (fills > i) mbar_wait_bounded(&full[i], (uint32_t)((fills - 1 - i) / stages) & 1u, err);
+    }
+    pdl_launch_dependents();   // rmsnorm_dweight_kernel may be scheduled; it waits for this kernel's end
     if (partial) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
@@ -223,12 +286,13 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
 // 32nd partial row each, then the warps' sums in warp order.
 __global__ void __launch_bounds__(1024)
     rmsnorm_dweight_kernel(const float* __restrict__ partial, int blocks, int H, float* __restrict__ dweight) {
+    pdl_wait();
     __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
     float v = 0.0f;
     if (col < H) {
-#pragma unroll 4
+#pragma unroll 8
         for (int b = warp; b < blocks; b += 32) v += partial[(int64_t)b * H + col];
     }
     red[warp][lane] = v;
@@ -249,15 +313,48 @@ int row_threads(int H, int ch) {
 
 int bwd_chunks(int H) { return H <= 4096 ? 1 : H <= 8192 ? 2 : 4; }
 
-int64_t bwd_blocks(int64_t T, int H, int sms) {
-    const int ch = bwd_chunks(H);
-    const int rows = ch == 1 ? 4 : ch == 2 ? 2 : 1;
-    const int64_t need = (T + rows - 1) / rows;
-    const int64_t cap = 2 * (int64_t)sms;
-    return need < cap ? need : cap;
+int bwd_rows(int H) { return bwd_chunks(H) == 1 ? BwdRows<1>::value : 1; }
+
+// Blocks an SM and slots a block of the backward: about kBwdThreads threads an SM,
+// as many slots as fit beside each other (at least two, so that a copy is always
+// in flight).
+struct BwdShape {
+    int per_sm, stages;
+    size_t smem;
+};
+
+BwdShape bwd_shape(int H, bool has_dsum) {
+    const size_t slot = (has_dsum ? 3 : 2) * 2 * (size_t)H * bwd_rows(H);
+    BwdShape b;
+    b.per_sm = kBwdThreads / row_threads(H, bwd_chunks(H));
+    if (b.per_sm > 8) b.per_sm = 8;
+    if (b.per_sm < 1) b.per_sm = 1;
+    while (b.per_sm > 1 && kBwdSmem / b.per_sm < 2 * slot) --b.per_sm;
+    b.stages = (int)(kBwdSmem / b.per_sm / slot);
+    if (b.stages > kMaxStages) b.stages = kMaxStages;
+    b.smem = b.stages * slot;
+    return b;
+}
+
+int64_t bwd_blocks(int64_t T, int H, int per_sm, int sms) {
+    const int64_t cap = (int64_t)per_sm * sms, groups = (T + bwd_rows(H) - 1) / bwd_rows(H);
+    return groups < cap ? groups : cap;
 }
 
 constexpr int kMaxSms = 256;   // bounds the workspace whatever the GPU
+
+template <int CH>
+cudaError_t launch_bwd(const bf16* dy, const bf16* s, const bf16* weight, const float* rstd, const bf16* dsum, int64_t T,
+                       int H, bf16* dx, float* partial, int64_t blocks, const BwdShape& b, cudaStream_t st,
+                       unsigned* err) {
+    auto kern = rmsnorm_backward_kernel<CH>;
+    // per device, so set on every call (a host-side table write)
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBwdSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)blocks, row_threads(H, CH), b.smem, st>>>(dy, s, reinterpret_cast<const uint4*>(weight), rstd, dsum,
+                                                               T, H, reinterpret_cast<uint4*>(dx), partial, b.stages, err);
+    return cudaGetLastError();
+}
 
 }  // namespace
 
@@ -267,40 +364,42 @@ cudaError_t launch_rmsnorm(const bf16* x, const bf16* residual, const bf16* weig
     const int chunks = H / 8;
     auto go = [&](auto kern, dim3 grid, int threads) {
         kern<<<grid, threads, 0, st>>>(reinterpret_cast<const uint4*>(x), reinterpret_cast<const uint4*>(residual),
-                                       reinterpret_cast<const uint4*>(weight), T, H, eps,
+                                       reinterpret_cast<const uint4*>(weight), H, eps,
                                        reinterpret_cast<uint4*>(sum), reinterpret_cast<uint4*>(y), y_q, y_scale, rstd);
     };
     const dim3 rows((unsigned)T);
-    if (chunks <= 512) go(rmsnorm_kernel<1, false>, rows, row_threads(H, 1));
-    else if (chunks <= 1024) go(rmsnorm_kernel<2, false>, rows, row_threads(H, 2));
-    else go(rmsnorm_kernel<4, false>, rows, row_threads(H, 4));
+    // More columns a thread keep more loads in flight an SM: 16384 rows of 5120 take
+    // 133, 127 and 122 us with 1, 2 and 4 chunks a thread, 4096 rows of 2048 14.3,
+    // 13.4 and 13.3. With fewer rows than SMs only the latency of one row counts
+    // (2.2, 2.4 and 3.2 us): as many threads as a block may have.
+    const int ch = T < sm_count() ? (chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4)
+                                  : (chunks <= 128 ? 1 : chunks <= 512 ? 2 : 4);
+    if (ch == 1) go(rmsnorm_kernel<1>, rows, row_threads(H, 1));
+    else if (ch == 2) go(rmsnorm_kernel<2>, rows, row_threads(H, 2));
+    else go(rmsnorm_kernel<4>, rows, row_threads(H, 4));
     return cudaGetLastError();
 }
 
 size_t rmsnorm_backward_workspace_bytes(int64_t T, int H) {
-    return (size_t)bwd_blocks(T, H, kMaxSms) * (size_t)H * sizeof(float);
+    const int a = bwd_shape(H, true).per_sm, b = bwd_shape(H, false).per_sm;
+    return (size_t)bwd_blocks(T, H, a > b ? a : b, kMaxSms) * (size_t)H * sizeof(float);
 }
 
 cudaError_t launch_rmsnorm_backward(const bf16* dy, const bf16* s, const bf16* weight, const float* rstd,
                                     const bf16* dsum, int64_t T, int H, bf16* dx, float* dweight, float* partial,
-                                    cudaStream_t st) {
+                                    cudaStream_t st, unsigned* err) {
     if (T == 0) return dweight ? cudaMemsetAsync(dweight, 0, sizeof(float) * (size_t)H, st) : cudaSuccess;
-    const int sms = sm_count() < kMaxSms ? sm_count() : kMaxSms;
-    const int64_t blocks = bwd_blocks(T, H, sms);
+    const BwdShape b = bwd_shape(H, dsum != nullptr);
+    const int64_t blocks = bwd_blocks(T, H, b.per_sm, sm_count() < kMaxSms ? sm_count() : kMaxSms);
+    if (!dweight) partial = nullptr;
     const int ch = bwd_chunks(H);
-    auto go = [&](auto kern) {
-        kern<<<(unsigned)blocks, row_threads(H, ch), 0, st>>>(
-            reinterpret_cast<const uint4*>(dy), reinterpret_cast<const uint4*>(s),
-            reinterpret_cast<const uint4*>(weight), rstd, reinterpret_cast<const uint4*>(dsum), T, H,
-            reinterpret_cast<uint4*>(dx), dweight ? partial : nullptr);
-    };
-    if (ch == 1) go(rmsnorm_backward_kernel<1>);
-    else if (ch == 2) go(rmsnorm_backward_kernel<2>);
-    else go(rmsnorm_backward_kernel<4>);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = ch == 1   ? launch_bwd<1>(dy, s, weight, rstd, dsum, T, H, dx, partial, blocks, b, st, err)
+                    : ch == 2 ? launch_bwd<2>(dy, s, weight, rstd, dsum, T, H, dx, partial, blocks, b, st, err)
+                              : launch_bwd<4>(dy, s, weight, rstd, dsum, T, H, dx, partial, blocks, b, st, err);
     if (e == cudaSuccess && dweight) {
-        rmsnorm_dweight_kernel<<<(unsigned)((H + 31) / 32), 1024, 0, st>>>(partial, (int)blocks, H, dweight);
-        e = cudaGetLastError();
+        const ChainScope chain(true);   // its launch and prologue overlap the last blocks' rows
+        e = launch_chained(rmsnorm_dweight_kernel, dim3((unsigned)((H + 31) / 32)), dim3(1024), 0, st,
+                           static_cast<const float*>(partial), (int)blocks, H, dweight);
     }
     return e;
 }
