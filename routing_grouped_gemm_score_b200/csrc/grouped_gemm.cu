@@ -107,6 +107,11 @@ struct Params {
     // lane holds a row: a warp's 32 bytes of one block are one sector.
     uint8_t* gu8;
     uint8_t* gu8_scale;
+    int64_t gu8_rows;
+    // kEpiSwigluBwd8, whose row blocks (offsets) are padded: the blocks of the rows
+    // of gu8. Row r of block g has g and u if r - offsets[g] < gu8_offsets[g + 1] -
+    // gu8_offsets[g]; the others are zero rows
+    const int32_t* gu8_offsets;
     int I;                     // SwiGLU: offset of the up half in [g | u]
     int tma_out, tma_out2;     // single-CTA kernel: out / out2 have TMA store maps
     const float* row_scale;    // SwiGLU forward: h[r] *= row_scale[r]; backward: ds = row_scale[r] * dh (NULL: 1)
@@ -194,6 +199,7 @@ __device__ __forceinline__ float silu_f(float g) { return g / (1.0f + expf(-g));
 
 struct Tile {
     int g, m_blk, n_blk;
+    int first;  // group-M: first row of the expert
     int row0;   // group-M: first A/output row of the tile; group-K: first X/D row of the expert
     int rows;   // group-M: valid rows of this tile; group-K: rows (K extent) of the expert
     int num_kb;
@@ -251,7 +257,7 @@ __device__ __forceinline__ void build_schedule(S& s, const Params& p, int bm) {
 template <bool GROUP_K, class S>
 __device__ __forceinline__ Tile decode_tile(const S& s, const Params& p, int id, int bm) {
     Tile t;
-    if (GROUP_K) {
+    if constexpr (GROUP_K) {
         const int per = p.m_blocks * p.n_blocks;
         t.g = id / per;
         const int local = id - t.g * per;
@@ -273,7 +279,8 @@ __device__ __forceinline__ Tile decode_tile(const S& s, const Params& p, int id,
         const int local = id - s.tile_start[t.g];
         t.n_blk = local / mt;
         t.m_blk = local - t.n_blk * mt;
-        t.row0 = s.off[t.g] + t.m_blk * bm;
+        t.first = s.off[t.g];
+        t.row0 = t.first + t.m_blk * bm;
         t.rows = min(bm, cnt - t.m_blk * bm);
         t.num_kb = (p.K + BK - 1) / BK;
     }
@@ -432,9 +439,9 @@ struct Aux8 {
 __device__ __forceinline__ void load_aux8(const Params& p, int64_t grow, int col, bool ok, Aux8& a) {
     if (!ok) return;
     const uint8_t* row = p.gu8 + grow * 2 * p.I + col;
-    const uint8_t* sc = p.gu8_scale + (int64_t)(col / kRows8Block) * p.rows + grow;
+    const uint8_t* sc = p.gu8_scale + (int64_t)(col / kRows8Block) * p.gu8_rows + grow;
     a.g_byte = __ldg(sc);
-    a.u_byte = __ldg(sc + (int64_t)rows8_blocks(p.I) * p.rows);
+    a.u_byte = __ldg(sc + (int64_t)rows8_blocks(p.I) * p.gu8_rows);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const bool in = col + 8 * q < p.I;
@@ -443,20 +450,35 @@ __device__ __forceinline__ void load_aux8(const Params& p, int64_t grow, int col
     }
 }
 
-// What an epilogue warp loads ahead of its accumulator.
+// What an epilogue warp loads ahead of its accumulator for row r of the tile
+// (nothing for other epilogues): the SwiGLU backward's g and u.
+struct AuxNone {};
 template <int EPI>
 struct EpiAux {
+    using type = AuxNone;
+};
+template <>
+struct EpiAux<kEpiSwigluBwd> {
     using type = Aux32;
 };
 template <>
 struct EpiAux<kEpiSwigluBwd8> {
-    using type = Aux8;
+    struct type {
+        Aux8 a;
+        int64_t row;   // of gu8, -1: a row past the block or a zero row
+    };
 };
 template <int EPI>
-__device__ __forceinline__ void load_epi_aux(const Params& p, int64_t grow, int col, bool ok,
+__device__ __forceinline__ void load_epi_aux(const Params& p, const Tile& t, int r, int col,
                                              typename EpiAux<EPI>::type& a) {
-    if constexpr (EPI == kEpiSwigluBwd8) load_aux8(p, grow, col, ok, a);
-    else load_aux32(p, grow, col, ok, a);
+    if constexpr (EPI == kEpiSwigluBwd) {
+        load_aux32(p, (int64_t)t.row0 + r, col, r < t.rows && col < p.N, a);
+    } else if constexpr (EPI == kEpiSwigluBwd8) {
+        const int begin = __ldg(p.gu8_offsets + t.g), end = __ldg(p.gu8_offsets + t.g + 1);
+        const int64_t row = (int64_t)begin + (t.row0 - t.first) + r;
+        a.row = r < t.rows && row >= 0 && row < end && row < p.gu8_rows ? row : -1;
+        load_aux8(p, a.row, col, a.row >= 0 && col < p.N, a.a);
+    }
 }
 
 // SwiGLU backward of one block of 32 columns from the 8-bit g and u, with the
@@ -621,9 +643,9 @@ __device__ __forceinline__ void epilogue_tile(const Params& p, const Tile& t, ui
             if (p.gu8 && lane < nvalid) {
                 // one rounding, from the fp32 accumulator
                 uint8_t* q = p.gu8 + (row0 + lane) * 2 * p.I + n0 + c0;
-                uint8_t* sc = p.gu8_scale + (int64_t)((n0 + c0) / kRows8Block) * p.rows + row0 + lane;
+                uint8_t* sc = p.gu8_scale + (int64_t)((n0 + c0) / kRows8Block) * p.gu8_rows + row0 + lane;
                 store_block8(q, sc, ncols, g);
-                store_block8(q + p.I, sc + (int64_t)rows8_blocks(p.I) * p.rows, ncols, u);
+                store_block8(q + p.I, sc + (int64_t)rows8_blocks(p.I) * p.gu8_rows, ncols, u);
             }
 #pragma unroll
             for (int i = 0; i < 32; ++i) g[i] = silu_f(g[i]) * u[i] * rs;     // h, in place
@@ -672,14 +694,16 @@ __device__ __forceinline__ void epilogue_tile(const Params& p, const Tile& t, ui
                                (int)row0);
         }
     } else if constexpr (EPI == kEpiSwigluBwd8) {
-        // as kEpiSwigluBwd, from the 8-bit g and u, with h stored as well (out2)
+        // as kEpiSwigluBwd, from the 8-bit g and u, with h stored as well (out2). The
+        // zero rows that pad a block get zeros, whatever the accumulator holds there
+        // (zeros times a weight that is not finite are not zeros).
         const int n0 = t.n_blk * n_tile;
-        const bool valid = r < t.rows;
         const int nvalid = min(max(t.rows - warp_r0, 0), 32);
-        const int64_t grow = (int64_t)t.row0 + r;
         const int64_t row0 = (int64_t)t.row0 + warp_r0;
-        Aux8& ax = *pre;
-        const float ps = valid ? __ldg(p.row_scale + grow) : 0.0f;
+        const int64_t grow = pre->row;
+        const bool real = grow >= 0;
+        Aux8& ax = pre->a;   // reloaded in place for each later chunk
+        const float ps = real ? __ldg(p.row_scale + row0 + lane) : 0.0f;
         float dot = 0.0f;
 #pragma unroll 1
         for (int ci = 0; ci < em.chunks; ++ci) {
@@ -689,17 +713,17 @@ __device__ __forceinline__ void epilogue_tile(const Params& p, const Tile& t, ui
             if (col >= p.N) continue;
             const int ncols = min(32, p.N - col);
             uint32_t dgp[16], dup[16], hp[16];
-            if (valid) {
+            if (real) {
                 swiglu_bwd8(dh, ax, ps, dot, dgp, dup, hp);
                 if ((ci & 1) || col + 32 >= p.N) {   // the 64-column group's last chunk
-                    p.row_dot[grow * p.ld_row_dot + (col >> 6)] = dot;
+                    p.row_dot[(row0 + lane) * p.ld_row_dot + (col >> 6)] = dot;
                     dot = 0.0f;
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) dgp[i] = dup[i] = hp[i] = 0u;   // rows past the block: not stored
+                for (int i = 0; i < 16; ++i) dgp[i] = dup[i] = hp[i] = 0u;
             }
-            load_aux8(p, grow, col + 32, valid && ci + 1 < em.chunks && col + 32 < p.N, ax);
+            load_aux8(p, grow, col + 32, real && ci + 1 < em.chunks && col + 32 < p.N, ax);
             put_block32_packed(buf, p.out + row0 * p.ldo + col, p.ldo, nvalid, ncols, dgp, lane, tmC, col,
                                (int)row0);
             put_block32_packed(buf, p.out + row0 * p.ldo + p.I + col, p.ldo, nvalid, ncols, dup, lane, tmC, p.I + col,
@@ -954,10 +978,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t use = (uint32_t)(local_tile >> 1);
             const EpiMap em = t.rows <= 128 ? em_half : em_full;   // a copy: a reference would need memory
             typename EpiAux<EPI>::type pre;
-            if (EPI == kEpiSwigluBwd || EPI == kEpiSwigluBwd8) {
-                const int col = t.n_blk * BN + em.c_lo;
-                load_epi_aux<EPI>(p, (int64_t)t.row0 + em.r0 + lane, col, em.r0 + lane < t.rows && col < p.N, pre);
-            }
+            load_epi_aux<EPI>(p, t, em.r0 + lane, t.n_blk * BN + em.c_lo, pre);
             if (!mbar_wait(&s.acc_full[buf], use & 1u, abort_flag, p.err)) break;
             tc_fence_after();
             const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BN);
@@ -965,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       p.tma_out ? &tmC : nullptr, p.tma_out2 ? &tmC2 : nullptr, &pre);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(leader_acc_empty(buf));
+            if (lane == 0) mbar_arrive_cluster_relaxed(leader_acc_empty(buf));
         }
         if (lane == 0) bulk_wait_group0();   // this warp's TMA stores have completed
         __syncwarp();
@@ -1238,10 +1259,7 @@ __global__ void __launch_bounds__(GROUP_K ? kThreadsK : kThreads, 1)
             const int buf = local_tile & 1;
             const uint32_t use = (uint32_t)(local_tile >> 1);
             typename EpiAux<EPI>::type pre;
-            if (EPI == kEpiSwigluBwd || EPI == kEpiSwigluBwd8) {
-                const int col = t.n_blk * BN + em.c_lo;
-                load_epi_aux<EPI>(p, (int64_t)t.row0 + warp_r0 + lane, col, warp_r0 + lane < t.rows && col < p.N, pre);
-            }
+            if constexpr (!GROUP_K) load_epi_aux<EPI>(p, t, warp_r0 + lane, t.n_blk * BN + em.c_lo, pre);
             if (!mbar_wait(&s.acc_full[buf], use & 1u, abort_flag, p.err)) break;
             tc_fence_after();
             const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BN);
@@ -1302,6 +1320,240 @@ __global__ void __launch_bounds__(GROUP_K ? kThreadsK : kThreads, 1)
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, kTmemCols);
+    }
+}
+
+// ============================================================ pair, group-K
+// gemm_wgrad_pair_kernel: the weight gradients dW[e] = X_e^T D_e on CTA pairs, for
+// row blocks that are padded with zero rows to multiples of 16 (a K step), so
+// that no slice holds rows of two experts in one K step.
+// A cluster computes a 256 x 256 block of dW[e] with tcgen05.mma.cta_group::2;
+// each CTA loads 128 columns of X and 128 of D per 64-row K slice, 32 KB for
+// 128 x 256 outputs where a single CTA's tile takes 48 KB, at the 64 bytes a cycle
+// that an SM takes from L2. The loads of both CTAs complete on the leader's full
+// barrier. Without the padding, each expert's last slice had to pass through a
+// warp per CTA that zeroed the rows past its end and released them to the
+// leader: about 1 us a tile, 274 against 262 us of the single-CTA kernel for the
+// Qwen3-30B-A3B gate_up gradient.
+// Shared memory of gemm_wgrad_pair_kernel: a ring of 5 stages, and two store
+// buffers of 32 rows x 64 columns per epilogue warp, so that a tile's stores have
+// the whole next tile to be read out. (With one buffer of 32 x 32 the epilogue
+// waited for its own stores: 308 us for the Qwen3-30B-A3B gate_up gradient.)
+constexpr int STAGESW = 5;
+struct __align__(1024) SmemW {
+    uint8_t stage[STAGESW][kStageP];
+    uint8_t epi[kEpiWarps][2][32 * 128];   // 128-byte-swizzled, as the store map reads them
+    uint64_t full[STAGESW];
+    uint64_t empty[STAGESW];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    int off[kMaxGroups + 1];
+};
+constexpr size_t kSmemWBytes = sizeof(SmemW) + 1024;
+static_assert(kSmemWBytes <= 227 * 1024, "shared memory per CTA");
+
+// Rows of slice kb are all whole 16-row K steps of the expert.
+__device__ __forceinline__ bool ragged_slice(const Tile& t, int kb) {
+    const int valid = t.rows - kb * BK;
+    return valid < BK && (valid & 15) != 0;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                           const __grid_constant__ CUtensorMap tmC, const Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    SmemW& s = *reinterpret_cast<SmemW*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();      // 0: leader, 1: peer
+    const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+    volatile int* abort_flag = &s.abort;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGESW; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.acc_full[i], 1);
+            mbar_init(&s.acc_empty[i], 2 * kEpiWarps);   // one arrival per epilogue warp of both CTAs
+        }
+        mbar_init(&s.drain, 1);
+        s.abort = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(&s.tmem_base, kTmemCols);
+        tmem_relinquish_pair();
+    }
+    pdl_wait();                // the previous kernel's outputs (X, D, offsets) are complete
+    for (int g = threadIdx.x; g <= p.groups; g += blockDim.x) s.off[g] = min(max(__ldg(p.offsets + g), 0), p.rows);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();        // barriers of both CTAs initialised, TMEM allocated
+    tc_fence_after();
+    const uint32_t tmem_base = s.tmem_base;
+    const int total = p.groups * p.m_blocks * p.n_blocks;
+
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            const uint64_t keep = l2_policy_evict_last();   // both panels are read again by other tiles
+            int stage = 0;
+            uint32_t phase = 0;
+            uint32_t loads = 0;   // stage loads issued; load j used stage j % STAGESW
+            bool ok = true;
+            for (int id = cluster; id < total && ok; id += clusters) {
+                const Tile t = decode_tile<true>(s, p, id, BMP);
+                const int m0 = t.m_blk * BMP + (int)rank * 128, n0 = t.n_blk * BN + (int)rank * 128;
+                for (int kb = 0; kb < t.num_kb; ++kb) {
+                    if (!mbar_wait(&s.empty[stage], phase ^ 1u, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* a_s = s.stage[stage];
+                    uint8_t* b_s = s.stage[stage] + kStageAP;
+                    const int krow = t.row0 + kb * BK;
+                    const uint32_t bar = mapa_shared(smem_u32(&s.full[stage]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&s.full[stage], 2 * kStageP);
+                    ++loads;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        tma_load_2d_pair_hint(&tmA, bar, a_s + c * kChunkBytes, m0 + 64 * c, krow, keep);
+                        tma_load_2d_pair_hint(&tmB, bar, b_s + c * kChunkBytes, n0 + 64 * c, krow, keep);
+                    }
+                    if (++stage == STAGESW) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // the leader waits for every load it armed to land before it may exit
+            if (rank == 0)
+                for (int i = 0; i < STAGESW; ++i)
+                    if (loads > (uint32_t)i)   // the stage's last load is its ((loads - 1 - i) / S)-th use
+                        mbar_wait(&s.full[i], ((loads - 1 - (uint32_t)i) / STAGESW) & 1u, abort_flag, p.err);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------ MMA issuer (leader)
+        if (rank == 0) {
+            constexpr uint32_t idesc = instr_desc<BMP, BN, true, true>();
+            int stage = 0;
+            uint32_t phase = 0;
+            int local_tile = 0;
+            bool ok = true;
+            bool any_mma = false;
+            for (int id = cluster; id < total && ok; id += clusters, ++local_tile) {
+                const Tile t = decode_tile<true>(s, p, id, BMP);
+                const int buf = local_tile & 1;
+                const uint32_t use = (uint32_t)(local_tile >> 1);
+                if (!mbar_wait_cluster(&s.acc_empty[buf], (use & 1u) ^ 1u, abort_flag, p.err)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(buf * BN);
+                if (t.num_kb == 0) {   // an expert without rows: the epilogues write zeros
+                    if (lane == 0) {
+                        mbar_arrive_cluster(mapa_shared(smem_u32(&s.acc_full[buf]), 0));
+                        mbar_arrive_cluster(mapa_shared(smem_u32(&s.acc_full[buf]), 1));
+                    }
+                    __syncwarp();
+                    continue;
+                }
+                for (int kb = 0; kb < t.num_kb; ++kb) {
+                    if (!mbar_wait(&s.full[stage], phase, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a_addr = smem_u32(s.stage[stage]);
+                    const uint32_t b_addr = a_addr + kStageAP;
+                    // the last slice: only the K steps that the expert's (padded) rows fill
+                    const int ksteps = min((t.rows - kb * BK + 15) / 16, BK / 16);
+                    if (lane == 0) {
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk) {
+                            if (kk >= ksteps) break;
+                            umma_bf16_pair(d_tmem, smem_desc(a_addr + kk * 2048, kChunkBytes, 1024),
+                                           smem_desc(b_addr + kk * 2048, kChunkBytes, 1024), idesc,
+                                           (kb | kk) != 0 ? 1u : 0u);
+                        }
+                        umma_commit_pair_mc(&s.empty[stage], 0x3);
+                        any_mma = true;
+                    }
+                    __syncwarp();
+                    if (++stage == STAGESW) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (lane == 0) umma_commit_pair_mc(&s.acc_full[buf], 0x3);
+                __syncwarp();
+            }
+            if (lane == 0 && any_mma) {
+                umma_commit_pair_mc(&s.drain, 0x1);
+                mbar_wait(&s.drain, 0, abort_flag, p.err);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------------ epilogue (both CTAs)
+        const int quarter = warp & 3;                           // TMEM lanes 32*quarter .. +31
+        const int col_half = (warp - 2) / 4;
+        uint32_t stores = 0;   // of this warp; store j uses buffer j & 1
+        int local_tile = 0;
+        for (int id = cluster; id < total; id += clusters, ++local_tile) {
+            const Tile t = decode_tile<true>(s, p, id, BMP);
+            const int acc = local_tile & 1;
+            const uint32_t use = (uint32_t)(local_tile >> 1);
+            if (!mbar_wait(&s.acc_full[acc], use & 1u, abort_flag, p.err)) break;
+            tc_fence_after();
+            const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN);
+            const int m0 = t.m_blk * BMP + (int)rank * 128 + quarter * 32;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {   // 64 columns at a time
+                const int c0 = 128 * col_half + 64 * i, n0 = t.n_blk * BN + c0;
+                float v[64];
+                if (t.num_kb > 0) {
+                    tmem_load_2x32(t_row + (uint32_t)c0, t_row + (uint32_t)c0 + 32,
+                                   *reinterpret_cast<float(*)[32]>(v), *reinterpret_cast<float(*)[32]>(v + 32));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+                }
+                if (n0 >= p.N || m0 >= p.M) continue;   // the store map drops rows past M and columns past N
+                uint8_t* buf = s.epi[warp - 2][stores++ & 1];
+                if (lane == 0) bulk_wait_group_read1();   // this buffer's last store has been read out
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                        make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                                   pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(&tmC, buf, n0, m0, t.g);
+                    bulk_commit_group();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&s.acc_empty[acc]), 0));
+        }
+        if (lane == 0) bulk_wait_group0();   // this warp's TMA stores have completed
+        __syncwarp();
+    }
+
+    pdl_launch_dependents();   // every role has left its loop (see gemm_pair_kernel)
+    tc_fence_before();
+    cluster_sync_all();        // no MMA, load or remote arrival of either CTA is still pending
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, kTmemCols);
     }
 }
 
@@ -1402,7 +1654,7 @@ __device__ __forceinline__ bool swap_epi_swiglu(SmemS<NR>& s, const Params& p, c
         // The warp's 32 lanes hold one block of 32 columns of every row. Its
         // largest finite magnitude: bit patterns of non-negative floats order as
         // the floats do, so an integer maximum over the warp finds it.
-        uint8_t* sc = p.gu8_scale + (int64_t)(t.n_blk * 2 + quarter) * p.rows + r0;
+        uint8_t* sc = p.gu8_scale + (int64_t)(t.n_blk * 2 + quarter) * p.gu8_rows + r0;
 #pragma unroll
         for (int i = 0; i < kWC; ++i) {
             if (i >= nvalid) break;   // the same for every lane
@@ -1414,7 +1666,7 @@ __device__ __forceinline__ bool swap_epi_swiglu(SmemS<NR>& s, const Params& p, c
                 if (hc >= p.N) continue;
                 p.gu8[(r0 + i) * 2 * p.I + half * p.I + hc] =
                     (uint8_t)(rows8_pack2(rows8_scaled_special(x, byte), 0.0f) & 0xFFu);
-                if (lane == 0) sc[(int64_t)half * rows8_blocks(p.I) * p.rows + i] = (uint8_t)byte;
+                if (lane == 0) sc[(int64_t)half * rows8_blocks(p.I) * p.gu8_rows + i] = (uint8_t)byte;
             }
         }
     }
@@ -2015,6 +2267,39 @@ bool use_swap_tiles(int64_t rows, int groups) {
     return rows <= (int64_t)groups * 16;
 }
 
+// Launches a kernel of CTA pairs (clusters of two), chained as launch_chained.
+template <class... KArgs, class... Args>
+cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t max_tiles, int threads, size_t smem, cudaStream_t st,
+                            Args&&... args) {
+    int64_t clusters = sm_count() / 2;
+    if (clusters > max_tiles) clusters = max_tiles;
+    if (clusters < 1) clusters = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * clusters));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeClusterDimension;
+    attrs[0].val.clusterDim.x = 2;
+    attrs[0].val.clusterDim.y = 1;
+    attrs[0].val.clusterDim.z = 1;
+    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[1].val.programmaticStreamSerializationAllowed = chained_launches() ? 1 : 0;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+}
+
+cudaError_t launch_wgrad_pair(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const Params& p,
+                              int64_t max_tiles, cudaStream_t st) {
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    if (set_smem_once(gemm_wgrad_pair_kernel, kSmemWBytes, once, attr) != cudaSuccess) return attr;
+    if (max_tiles <= 0) return cudaSuccess;
+    return launch_clusters(gemm_wgrad_pair_kernel, max_tiles, kThreads, kSmemWBytes, st, a, b, c, p);
+}
+
 template <int NR>
 cudaError_t launch_mlp(const CUtensorMap& x_rows, const CUtensorMap& w_gate_up, const CUtensorMap& h_rows,
                        const CUtensorMap& w_down, const Params& p, int64_t grid, cudaStream_t st) {
@@ -2100,6 +2385,7 @@ cudaError_t gemm_gate_up_swiglu(const bf16* x, int64_t rows, const int32_t* offs
     p.ldo2 = 2 * (int64_t)I;
     p.gu8 = gu8.q;
     p.gu8_scale = gu8.scale;
+    p.gu8_rows = rows;
     p.row_scale = row_scale;
     if (use_swap_tiles(rows, groups)) {
         p.n_blocks = (I + 63) / 64;   // 64 gate and the matching 64 up columns per tile
@@ -2133,6 +2419,7 @@ cudaError_t gemm_gate_up_swiglu_gather(const bf16* x, int64_t T, const int32_t* 
     p.ldo2 = 2 * (int64_t)I;
     p.gu8 = gu8.q;
     p.gu8_scale = gu8.scale;
+    p.gu8_rows = rows;
     p.row_scale = row_scale;
     p.gather_x = x;
     p.gather_tok = sorted_token;
@@ -2182,6 +2469,7 @@ cudaError_t gemm_expert_mlp_fused(const bf16* x, int64_t rows, const int32_t* of
     p.ldo2 = 2 * (int64_t)I;
     p.gu8 = gu8.q;
     p.gu8_scale = gu8.scale;
+    p.gu8_rows = rows;
     p.y = y;
     p.ldy = H;
     p.N2 = H;
@@ -2283,8 +2571,9 @@ cudaError_t gemm_down_dgrad_swiglu(const bf16* dy, int64_t rows, const int32_t* 
 }
 
 cudaError_t gemm_down_dgrad_swiglu8(const bf16* dy, int64_t rows, const int32_t* offsets, int E, int H, int I,
-                                    const bf16* w_down, const Rows8& gu8, const float* row_scale, bf16* dgu, bf16* h,
-                                    float* row_dot, cudaStream_t st, unsigned* err) {
+                                    const bf16* w_down, const Rows8& gu8, int64_t gu8_rows, const int32_t* gu8_offsets,
+                                    const float* row_scale, bf16* dgu, bf16* h, float* row_dot, cudaStream_t st,
+                                    unsigned* err) {
     if (rows == 0) return cudaSuccess;
     CUtensorMap ta, ta64, tb, tb1;   // as in gemm_down_dgrad_swiglu
     if (!make_map_2d(&ta, dy, H, rows, H, BK, 128)) return cudaErrorInvalidValue;
@@ -2302,6 +2591,8 @@ cudaError_t gemm_down_dgrad_swiglu8(const bf16* dy, int64_t rows, const int32_t*
     p.ldo2 = I;
     p.gu8 = gu8.q;
     p.gu8_scale = gu8.scale;
+    p.gu8_rows = gu8_rows;
+    p.gu8_offsets = gu8_offsets;
     p.row_scale = row_scale;
     p.row_dot = row_dot;
     p.ld_row_dot = (I + 63) / 64;
@@ -2337,7 +2628,7 @@ cudaError_t gemm_gate_up_dgrad(const bf16* dgu, int64_t rows, const int32_t* off
 }
 
 cudaError_t gemm_wgrad(const bf16* X, const bf16* D, int64_t rows, const int32_t* offsets, int E,
-                       int M, int N, bf16* dW, cudaStream_t st, unsigned* err) {
+                       int M, int N, bf16* dW, cudaStream_t st, unsigned* err, bool blocks16) {
     CUtensorMap ta, tb;
     const uint64_t r = rows > 0 ? (uint64_t)rows : 1;  // an empty X still needs a valid map
     if (!make_map_2d(&ta, X, M, r, M, 64, BK)) return cudaErrorInvalidValue;
@@ -2345,14 +2636,18 @@ cudaError_t gemm_wgrad(const bf16* X, const bf16* D, int64_t rows, const int32_t
     Params p = base_params(E, rows, offsets, err);
     p.M = M;
     p.N = N;
-    p.m_blocks = (M + BM1 - 1) / BM1;
+    const bool pair = blocks16 && M > BM1;
+    const int m_tile = pair ? BMP : BM1;
+    p.m_blocks = (M + m_tile - 1) / m_tile;
     p.n_blocks = (N + BN - 1) / BN;
     p.out = dW;
     p.ldo = N;
     p.out_group_stride = (int64_t)M * N;
-    CUtensorMap tc;   // dW [E][M][N], stored in 32 x 32 blocks without swizzle
-    if (!make_map_3d(&tc, dW, N, M, E > 0 ? E : 1, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    CUtensorMap tc;   // dW [E][M][N], stored in blocks of 32 rows
+    if (!make_map_3d(&tc, dW, N, M, E > 0 ? E : 1, pair ? 64 : 32, 32,
+                     pair ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
         return cudaErrorInvalidValue;
+    if (pair) return launch_wgrad_pair(ta, tb, tc, p, (int64_t)E * p.m_blocks * p.n_blocks, st);
     // One 128 x 256 tile per CTA at a time. A kernel that kept each expert's
     // B rows in shared memory across M blocks measured slower at the
     // Qwen3-30B-A3B shape (313 against 288 us for the gate_up gradient): its

@@ -147,23 +147,28 @@ BwdLayout bwd_layout(void* ws, int64_t T, int H, int I, int k) {
     return L;
 }
 
-// The backward from the 8-bit state. One [A][H] buffer serves in turn as dy (the
+// The backward from the 8-bit state, on expert blocks padded with zero rows to
+// multiples of 16 (R rows at most). One [R][H] buffer serves in turn as dy (the
 // rows of dout), dx by row, and x by row: each is dead before the next is written.
 struct Bwd8Layout {
+    int64_t R;
     bf16 *rows, *dgu, *h;
     float *prob_row, *row_dot;
+    int32_t *pad_offsets, *pad_row;
     size_t bytes;
 };
 
-Bwd8Layout bwd8_layout(void* ws, int64_t T, int H, int I, int k) {
-    const int64_t A = T * k;
+Bwd8Layout bwd8_layout(void* ws, int64_t T, int H, int I, int E, int k) {
     Carver c(ws);
     Bwd8Layout L;
-    L.rows = c.take<bf16>((size_t)A * H);
-    L.dgu = c.take<bf16>((size_t)A * 2 * I);
-    L.h = c.take<bf16>((size_t)A * I);
-    L.prob_row = c.take<float>((size_t)A);
-    L.row_dot = c.take<float>((size_t)A * ((I + 63) / 64));
+    L.R = pad16_rows(T * k, E);
+    L.rows = c.take<bf16>((size_t)L.R * H);
+    L.dgu = c.take<bf16>((size_t)L.R * 2 * I);
+    L.h = c.take<bf16>((size_t)L.R * I);
+    L.prob_row = c.take<float>((size_t)L.R);
+    L.row_dot = c.take<float>((size_t)L.R * ((I + 63) / 64));
+    L.pad_offsets = c.take<int32_t>((size_t)E + 1);
+    L.pad_row = c.take<int32_t>((size_t)(T * k));
     L.bytes = c.bytes();
     return L;
 }
@@ -836,8 +841,8 @@ moe_status moe_grouped_mlp_scaled_backward(const moe_bf16* dout, int64_t T, int 
 }
 
 size_t moe_grouped_mlp_backward_ckpt_workspace_size(int64_t T, int H, int I, int E, int k) {
-    if (!shape_ok(T, E, k) || !dims_ok(H, I)) return 0;
-    return bwd8_layout(nullptr, T, H, I, k).bytes;
+    if (!shape_ok(T, E, k) || !dims_ok(H, I) || pad16_rows(T * k, E) >= (int64_t(1) << 31)) return 0;
+    return bwd8_layout(nullptr, T, H, I, E, k).bytes;
 }
 
 moe_status moe_grouped_mlp_backward_ckpt(const moe_bf16* dout, int64_t T, int H, int I, int E, int k,
@@ -848,7 +853,7 @@ moe_status moe_grouped_mlp_backward_ckpt(const moe_bf16* dout, int64_t T, int H,
                                           void* workspace, size_t workspace_bytes, void* stream) {
     const ChainScope chain(T * (int64_t)k <= kChainMaxRows);
     if (!shape_ok(T, E, k) || H <= 0 || I <= 0) return MOE_ERR_INVALID_ARG;
-    if (!dims_ok(H, I)) return MOE_ERR_UNSUPPORTED;
+    if (!dims_ok(H, I) || pad16_rows(T * k, E) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
     if (!dw_gate_up || !dw_down || !aligned16(dw_gate_up) || !aligned16(dw_down)) return MOE_ERR_INVALID_ARG;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (T == 0) {   // no rows: only the weight gradients have elements, and they are zero
@@ -860,36 +865,39 @@ moe_status moe_grouped_mlp_backward_ckpt(const moe_bf16* dout, int64_t T, int H,
                           dprob};
     for (const void* p : must)
         if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
-    if (!workspace || !aligned16(workspace) || workspace_bytes < bwd8_layout(nullptr, T, H, I, k).bytes)
+    if (!workspace || !aligned16(workspace) || workspace_bytes < bwd8_layout(nullptr, T, H, I, E, k).bytes)
         return MOE_ERR_WORKSPACE;
     unsigned* err = device_error_word();
     if (!err) return MOE_ERR_CUDA;
-    const Bwd8Layout L = bwd8_layout(workspace, T, H, I, k);
+    const Bwd8Layout L = bwd8_layout(workspace, T, H, I, E, k);
     const int64_t A = T * k;
     auto B = [](const moe_bf16* p) { return reinterpret_cast<const bf16*>(p); };
     const Rows8 gu8{const_cast<uint8_t*>(gu_q), const_cast<uint8_t*>(gu_scale)};   // read only
+    const int32_t* blocks = L.pad_offsets;
     cudaError_t e = trace_mark(0, st);
     if (e == cudaSuccess)
-        e = launch_spread_rows(B(dout), row_of, topk_prob, T, k, H, A, L.rows, L.prob_row, st, err);
+        e = launch_spread_rows(B(dout), row_of, offsets, topk_prob, T, k, E, H, L.rows, L.prob_row, L.pad_offsets,
+                               L.pad_row, st, err);
     if (e == cudaSuccess) e = trace_mark(1, st);
     if (e == cudaSuccess)
-        e = gemm_down_dgrad_swiglu8(L.rows, A, offsets, E, H, I, B(w_down), gu8, L.prob_row, L.dgu, L.h, L.row_dot,
-                                    st, err);
-    if (e == cudaSuccess) e = launch_row_dot_sum(L.row_dot, (I + 63) / 64, row_of, A, A, dprob, st, err);
+        e = gemm_down_dgrad_swiglu8(L.rows, L.R, blocks, E, H, I, B(w_down), gu8, A, offsets, L.prob_row, L.dgu, L.h,
+                                    L.row_dot, st, err);
+    if (e == cudaSuccess) e = launch_row_dot_sum(L.row_dot, (I + 63) / 64, L.pad_row, A, L.R, dprob, st, err);
     if (e == cudaSuccess) e = trace_mark(2, st);
     if (e == cudaSuccess)
-        e = gemm_wgrad(L.h, L.rows, A, offsets, E, I, H, reinterpret_cast<bf16*>(dw_down), st, err);
+        e = gemm_wgrad(L.h, L.rows, L.R, blocks, E, I, H, reinterpret_cast<bf16*>(dw_down), st, err, true);
     if (e == cudaSuccess) e = trace_mark(3, st);
     // dy is done with: its buffer takes each row's dx, and then each row's x
     if (e == cudaSuccess)
-        e = gemm_gate_up_dgrad(L.dgu, A, offsets, E, H, I, B(w_gate_up), L.rows, st, err);
+        e = gemm_gate_up_dgrad(L.dgu, L.R, blocks, E, H, I, B(w_gate_up), L.rows, st, err);
     if (e == cudaSuccess) e = trace_mark(4, st);
     if (e == cudaSuccess)
-        e = launch_combine(L.rows, row_of, nullptr, T, k, H, A, nullptr, reinterpret_cast<bf16*>(dx), st, err);
+        e = launch_combine(L.rows, L.pad_row, nullptr, T, k, H, L.R, nullptr, reinterpret_cast<bf16*>(dx), st, err);
     if (e == cudaSuccess) e = trace_mark(5, st);
-    if (e == cudaSuccess) e = launch_spread_rows8(x_q, x_scale, row_of, T, k, H, A, L.rows, st, err);
     if (e == cudaSuccess)
-        e = gemm_wgrad(L.rows, L.dgu, A, offsets, E, H, 2 * I, reinterpret_cast<bf16*>(dw_gate_up), st, err);
+        e = launch_spread_rows8(x_q, x_scale, offsets, T, k, E, H, L.rows, L.pad_offsets, L.pad_row, st);
+    if (e == cudaSuccess)
+        e = gemm_wgrad(L.rows, L.dgu, L.R, blocks, E, H, 2 * I, reinterpret_cast<bf16*>(dw_gate_up), st, err, true);
     if (e == cudaSuccess) e = trace_mark(6, st);
     return from_cuda(e);
 }

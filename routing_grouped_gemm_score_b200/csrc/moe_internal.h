@@ -146,12 +146,19 @@ cudaError_t launch_quantize_rows(const bf16* x, int64_t rows, int cols, int part
                                  uint8_t* scale, cudaStream_t st);
 cudaError_t launch_dequantize_rows(const uint8_t* q, const uint8_t* scale, int64_t rows, int cols, int parts,
                                    int block_major, bf16* x, cudaStream_t st);
-// rows[row_of[t, j]] = src[t] for every assignment (and prob_row[row] = prob[t, j]
-// when prob_row is given); launch_spread_rows8 reads src from 8 bits.
-cudaError_t launch_spread_rows(const bf16* src, const int32_t* row_of, const float* prob, int64_t T, int k, int H,
-                               int64_t A, bf16* rows, float* prob_row, cudaStream_t st, unsigned* err);
-cudaError_t launch_spread_rows8(const uint8_t* q, const uint8_t* scale, const int32_t* row_of, int64_t T, int k,
-                                int H, int64_t A, bf16* rows, cudaStream_t st, unsigned* err);
+// The dispatches of the 8-bit checkpoint's backward, into row blocks padded with
+// zero rows to multiples of 16: pad_offsets [E + 1] and pad_row [T][k] (written by
+// the first) hold the blocks and each assignment's row. rows has A + 15 min(E, A)
+// rows (pad16_rows).
+constexpr int64_t pad16_rows(int64_t A, int E) { return A + 15 * (A < E ? A : (int64_t)E); }
+// rows[pad_row[t, j]] = src[t], prob_row[row] = prob[t, j] (0 in a zero row)
+cudaError_t launch_spread_rows(const bf16* src, const int32_t* row_of, const int32_t* offsets, const float* prob,
+                               int64_t T, int k, int E, int H, bf16* rows, float* prob_row, int32_t* pad_offsets,
+                               int32_t* pad_row, cudaStream_t st, unsigned* err);
+// the same rows from src in 8 bits, with pad_offsets and pad_row given
+cudaError_t launch_spread_rows8(const uint8_t* q, const uint8_t* scale, const int32_t* offsets, int64_t T, int k,
+                                int E, int H, bf16* rows, const int32_t* pad_offsets, const int32_t* pad_row,
+                                cudaStream_t st);
 
 // RMSNorm with the residual's addition, and its backward (rmsnorm.cu).
 constexpr int kRmsnormMaxH = 16384;
@@ -220,18 +227,23 @@ cudaError_t gemm_down_dgrad_swiglu(const bf16* dy, int64_t rows, const int32_t* 
                                    float* row_dot = nullptr);
 // dgrad of down with the SwiGLU backward from an 8-bit [g | u] (gu8 as above): as
 // gemm_down_dgrad_swiglu with row_scale and row_dot, and h[r] = row_scale[r] *
-// silu(g) * u, recomputed, for the down weight's gradient.
+// silu(g) * u, recomputed, for the down weight's gradient. The row blocks of dy and
+// of the outputs (offsets) may be padded; gu8's rows are those of gu8_offsets,
+// gu8_rows of them, and the rows past them in a block get zeros.
 cudaError_t gemm_down_dgrad_swiglu8(const bf16* dy, int64_t rows, const int32_t* offsets, int E, int H, int I,
-                                    const bf16* w_down, const Rows8& gu8, const float* row_scale, bf16* dgu, bf16* h,
-                                    float* row_dot, cudaStream_t st, unsigned* err);
+                                    const bf16* w_down, const Rows8& gu8, int64_t gu8_rows, const int32_t* gu8_offsets,
+                                    const float* row_scale, bf16* dgu, bf16* h, float* row_dot, cudaStream_t st,
+                                    unsigned* err);
 // dgrad of gate_up: dx_perm = dgu Wgu[e]^T
 cudaError_t gemm_gate_up_dgrad(const bf16* dgu, int64_t rows, const int32_t* offsets, int E, int H,
                                int I, const bf16* w_gate_up, bf16* dx_perm, cudaStream_t st,
                                unsigned* err);
 // wgrad: dW[e] = X_e^T D_e over the rows of group e (ragged reduction);
 // X [rows, M], D [rows, N], dW [E, M, N]. Empty groups get dW[e] = 0.
+// blocks16: every block is a multiple of 16 rows (zero rows at its end), which
+// lets it run on CTA pairs.
 cudaError_t gemm_wgrad(const bf16* X, const bf16* D, int64_t rows, const int32_t* offsets, int E,
-                       int M, int N, bf16* dW, cudaStream_t st, unsigned* err);
+                       int M, int N, bf16* dW, cudaStream_t st, unsigned* err, bool blocks16 = false);
 
 int sm_count();
 

@@ -1,6 +1,7 @@
 // rows8.cu -- rows in the 8-bit format of rows8.cuh: to it from bf16 and back,
 // and the two dispatches of the 8-bit checkpoint's backward, which write each
-// routed row's output gradient and its x, read back from the token's 8-bit row.
+// routed row's output gradient and its x, read back from the token's 8-bit row,
+// into expert blocks padded to whole K steps of 16 rows.
 //
 // All of them are bound by HBM bandwidth. A warp owns a unit of up to 1024
 // consecutive columns of one row (32 lanes x 4 chunks of 8 columns), its loads
@@ -14,6 +15,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxExperts = 256;
 constexpr int kChunks = 4;                   // 8-column chunks of a lane in one unit
 constexpr int kUnitChunks = 32 * kChunks;    // chunks of a unit (blocks of four chunks, padded)
 
@@ -115,35 +117,97 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// One token's row to the k rows that its assignments hold: rows[row_of[t, j]] =
-// the token's row, bf16 as it is (Q8 false) or read back from 8 bits (Q8 true).
-// Each token's row is read once. A warp owns a unit of one token's row; its
-// lanes hold the token's rows (lane j: row_of[t, j]). With prob given, the unit
-// of a token's first columns also writes prob_row[row] = prob[t, j]. A row
-// outside [0, A) is recorded and skipped.
+// The row blocks of the backward are padded with zero rows to multiples of 16, a
+// K step of the weight gradients: block e starts at pad[e] = sum over e' < e of
+// the counts rounded up. Both in shared memory; called by the whole block.
+struct PadBlocks {
+    int off[kMaxExperts + 1], pad[kMaxExperts + 1];
+    int warp_sum[kThreads / 32];
+};
+static_assert(kThreads >= kMaxExperts, "one thread per expert");
+
+__device__ __forceinline__ void pad_blocks(PadBlocks& b, const int32_t* __restrict__ offsets, int E, int64_t A) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = threadIdx.x;
+    for (int i = threadIdx.x; i <= E; i += kThreads) b.off[i] = (int)min(max((int64_t)__ldg(offsets + i), (int64_t)0), A);
+    __syncthreads();
+    int sum = e < E ? (max(b.off[e + 1] - b.off[e], 0) + 15) / 16 * 16 : 0;   // inclusive prefix
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += v;
+    }
+    if (lane == 31) b.warp_sum[warp] = sum;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) sum += b.warp_sum[w];
+    if (e < E) b.pad[e + 1] = sum;
+    if (e == 0) b.pad[0] = 0;
+    __syncthreads();
+}
+
+// Zero rows at the blocks' ends, a warp per row: rows (and prob_row, if given).
+__device__ __forceinline__ void zero_pad_rows(const int* off, const int* pad, int E, int chunks, int64_t bound,
+                                              uint4* rows, float* prob_row) {
+    const int lane = threadIdx.x & 31;
+    const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
+    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; i < 16 * (int64_t)E; i += nwarps) {
+        const int e = (int)(i >> 4);
+        const int64_t r = (int64_t)pad[e] + max(off[e + 1] - off[e], 0) + (i & 15);
+        if (r >= pad[e + 1] || r >= bound) continue;
+        for (int c = lane; c < chunks; c += 32) rows[r * chunks + c] = make_uint4(0, 0, 0, 0);
+        if (prob_row != nullptr && lane == 0) prob_row[r] = 0.0f;
+    }
+}
+
+// One token's row to the k rows that its assignments hold: bf16 as it is (Q8
+// false) or read back from 8 bits (Q8 true). Each token's row is read once. A
+// warp owns a unit of one token's row; lane j holds the row of assignment j.
+// Q8 false finds the padded rows: the expert of row_of[t, j] by bisection of the
+// blocks' offsets, then its place in the padded block. The unit of a token's
+// first columns writes pad_row and prob_row, and the first block pad_offsets. A
+// row outside its range is recorded and skipped (pad_row -1).
 template <bool Q8>
 __global__ void __launch_bounds__(kThreads)
     spread_rows_kernel(const void* __restrict__ src, const uint8_t* __restrict__ scale,
-                       const int32_t* __restrict__ row_of, const float* __restrict__ prob, int64_t T, int k, int H,
-                       int64_t A, bf16* __restrict__ rows, float* __restrict__ prob_row, unsigned* err) {
+                       const int32_t* __restrict__ row_of, const int32_t* __restrict__ offsets,
+                       const float* __restrict__ prob, int64_t T, int k, int E, int H, bf16* __restrict__ rows,
+                       float* __restrict__ prob_row, int32_t* pad_offsets, int32_t* pad_row, unsigned* err) {
+    __shared__ PadBlocks b;
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int chunks = H / 8, S = rows8_blocks(H);
     const int per_row = (chunks + kUnitChunks - 1) / kUnitChunks;
+    const int64_t A = T * k, bound = pad16_rows(A, E);
     const int64_t units = T * per_row, nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
+    pad_blocks(b, offsets, E, A);
+    if (!Q8 && blockIdx.x == 0)
+        for (int i = threadIdx.x; i <= E; i += kThreads) pad_offsets[i] = b.pad[i];
     for (int64_t u = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; u < units; u += nwarps) {
         int64_t t;
         int part;
         split_unit(u, per_row, t, part);
         int32_t mine = -1;
         if (lane < k) {
-            mine = __ldg(row_of + t * k + lane);
-            if (mine < 0 || mine >= A) {
-                raise_error(err, kErrDeviceCheck);
-                mine = -1;
+            if (Q8) {
+                mine = __ldg(pad_row + t * k + lane);
+            } else {
+                const int32_t row = __ldg(row_of + t * k + lane);
+                if (row >= 0 && row < A) {
+                    int lo = 0, hi = E - 1;   // last expert whose block starts at or before the row
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        if (b.off[mid] <= row) lo = mid;
+                        else hi = mid - 1;
+                    }
+                    const int64_t r = (int64_t)b.pad[lo] + (row - b.off[lo]);
+                    if (row >= b.off[lo] && row < b.off[lo + 1] && r < bound) mine = (int32_t)r;
+                }
+                if (mine < 0) raise_error(err, kErrDeviceCheck);
+                if (part == 0) {
+                    pad_row[t * k + lane] = mine;
+                    if (mine >= 0) prob_row[mine] = __ldg(prob + t * k + lane);
+                }
             }
-            if (prob_row != nullptr && part == 0 && mine >= 0) prob_row[mine] = __ldg(prob + t * k + lane);
         }
         uint4 v[kChunks];
 #pragma unroll
@@ -168,6 +232,7 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
     }
+    zero_pad_rows(b.off, b.pad, E, chunks, bound, reinterpret_cast<uint4*>(rows), Q8 ? nullptr : prob_row);
 }
 
 // Blocks for a warp-per-unit kernel: enough warps for every unit, at most what
@@ -198,22 +263,26 @@ cudaError_t launch_dequantize_rows(const uint8_t* q, const uint8_t* scale, int64
                           0, st, q, scale, rows, cols, parts, block_major, x);
 }
 
-cudaError_t launch_spread_rows(const bf16* src, const int32_t* row_of, const float* prob, int64_t T, int k, int H,
-                               int64_t A, bf16* rows, float* prob_row, cudaStream_t st, unsigned* err) {
+cudaError_t launch_spread_rows(const bf16* src, const int32_t* row_of, const int32_t* offsets, const float* prob,
+                               int64_t T, int k, int E, int H, bf16* rows, float* prob_row, int32_t* pad_offsets,
+                               int32_t* pad_row, cudaStream_t st, unsigned* err) {
     if (T == 0) return cudaSuccess;
     const int64_t units = T * ((H / 8 + kUnitChunks - 1) / kUnitChunks);
     return launch_chained(spread_rows_kernel<false>, dim3(unit_blocks(units)), dim3(kThreads), 0, st,
-                          static_cast<const void*>(src), static_cast<const uint8_t*>(nullptr), row_of, prob, T, k, H,
-                          A, rows, prob_row, err);
+                          static_cast<const void*>(src), static_cast<const uint8_t*>(nullptr), row_of, offsets, prob,
+                          T, k, E, H, rows, prob_row, pad_offsets, pad_row, err);
 }
 
-cudaError_t launch_spread_rows8(const uint8_t* q, const uint8_t* scale, const int32_t* row_of, int64_t T, int k,
-                                int H, int64_t A, bf16* rows, cudaStream_t st, unsigned* err) {
+cudaError_t launch_spread_rows8(const uint8_t* q, const uint8_t* scale, const int32_t* offsets, int64_t T, int k,
+                                int E, int H, bf16* rows, const int32_t* pad_offsets, const int32_t* pad_row,
+                                cudaStream_t st) {
     if (T == 0) return cudaSuccess;
     const int64_t units = T * ((H / 8 + kUnitChunks - 1) / kUnitChunks);
     return launch_chained(spread_rows_kernel<true>, dim3(unit_blocks(units)), dim3(kThreads), 0, st,
-                          static_cast<const void*>(q), scale, row_of, static_cast<const float*>(nullptr), T, k, H, A,
-                          rows, static_cast<float*>(nullptr), err);
+                          static_cast<const void*>(q), scale, static_cast<const int32_t*>(nullptr), offsets,
+                          static_cast<const float*>(nullptr), T, k, E, H, rows, static_cast<float*>(nullptr),
+                          const_cast<int32_t*>(pad_offsets), const_cast<int32_t*>(pad_row),
+                          static_cast<unsigned*>(nullptr));
 }
 
 }  // namespace moe
