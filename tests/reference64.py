@@ -135,16 +135,19 @@ def layer_backward(dout, x, gu, p, w_gate_up, w_down, row_of, offsets):
         s, silu = silu_parts(g)
         act = silu * u
         dh = dy @ w_down[e].T
-        # fp32 products of H terms; exp, the reciprocal and the few products after it: 8 fp32 roundings
+        # fp32 products of H terms; the sigmoid s: __expf is off by 2 + 1.173 |g| ulp (2 F32 each), which moves
+        # s by (1 - s) times that, __fdividef by 2 ulp; and the few products after it: 8 fp32 roundings
         dh_tol = H * TC * (dy.abs() @ w_down[e].abs().T)
-        few = 8 * F32
+        few = (8 + 2 * 2 + 2 * (2 + 1.173 * g.abs())) * F32
         dot[a:b] = (dh * act).sum(dim=1)
-        dot_tol[a:b] = (dh_tol * act.abs()).sum(dim=1) + (few + (64 + I // 64 + 2) * F32) * (dh * act).abs().sum(dim=1)
+        dot_tol[a:b] = (dh_tol * act.abs() + (few + (64 + I // 64 + 2) * F32) * (dh * act).abs()).sum(dim=1)
         slope = s + silu * (1 - s)
-        slope_abs = s + silu.abs() * (1 - s)
+        # s + silu (1 - s): relative to its terms; and the rounding of s (5 F32) passes through 1 - s
+        slope_tol = few * (s + silu.abs() * (1 - s)) + 5 * F32 * silu.abs() * s
         dgu = torch.cat([pe * dh * u * slope, pe * dh * silu], dim=1)
-        mag = torch.cat([pe * u.abs() * slope_abs, pe * silu.abs()], dim=1).abs()
-        dgu_tol = BF16 * dgu.abs() + mag * (dh_tol + few * dh.abs()).repeat(1, 2) * (1 + BF16)
+        from_dh = torch.cat([pe * u.abs() * slope.abs(), pe * silu.abs()], dim=1).abs() * dh_tol.repeat(1, 2)
+        from_s = torch.cat([pe * u.abs() * slope_tol, few * pe * silu.abs()], dim=1).abs() * (dh.abs() + dh_tol).repeat(1, 2)
+        dgu_tol = BF16 * dgu.abs() + (from_dh + from_s) * (1 + BF16)
         h, h_tol = pe * act, (BF16 + few) * (pe * act).abs()
         r["dw_down"][e] = h.T @ dy
         tol["dw_down"][e] = h_tol.T @ dy.abs() + n * TC * (h.abs().T @ dy.abs())
