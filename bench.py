@@ -70,6 +70,8 @@ def parse():
     ap.add_argument("--router-calls", type=int, default=None, metavar="LOGT",
                     help="only call the router three times at T = 2^LOGT, E=128, k=8 on N(0,1) logits "
                          "(a small program for ncu captures of the router), then exit")
+    ap.add_argument("--ckpt-compare", action="store_true",
+                    help="also the Qwen3 training step with the bf16 and with the 8-bit saved state")
     ap.add_argument("--scaled-compare", action="store_true",
                     help="also time the Qwen3-30B-A3B fwd+bwd with the routing weights applied "
                          "before FC2 (ScaledSwiGLU) on a padded dispatch, beside the default layer")
@@ -738,6 +740,8 @@ def our_arm(args, world, rank, local):
         line["router_sweep"] = router_sweep(m, hbm)
     if args.gather_compare:
         line["gather_compare"] = gather_compare(m)
+    if args.ckpt_compare:
+        line["ckpt_compare"] = ckpt_compare(m)
     if args.scaled_compare:
         line["scaled_compare"] = scaled_compare(m)
     if not args.no_cpu_baseline and world == 1 and rank == 0:
@@ -836,6 +840,59 @@ def router_sweep(m, hbm):
         out.append(entry)
         del logits, res, ws, dprob, dl, aws
     return out
+
+
+def ckpt_compare(m):
+    """The Qwen3-30B-A3B-shaped training step (T=4096, H=2048, I=768, E=128,
+    k=8, forward and backward), with a norm before it, on the two saved states:
+    bf16 (moe_layer_forward, moe_grouped_mlp_backward) and 8 bits
+    (moe_layer_forward_ckpt on the norm's 8-bit rows, moe_grouped_mlp_backward_ckpt).
+    L2 flushed before each step, CUDA events on the device, median of 10 after
+    3; and the bytes that each keeps between the passes."""
+    import torch
+    import workloads as wl
+    w = wl.WORKLOADS["qwen3_30b_a3b"]
+    d = wl.make_inputs(w, "cuda", with_dout=True)
+    opts = m.RouterOpts(w.score, w.renormalize)
+    flush = torch.ones(64 << 20, dtype=torch.float32, device="cuda")
+    weight = torch.ones(w.H, dtype=torch.bfloat16, device="cuda")
+    args = (d["w_gate_up"], d["w_down"], w.k, opts)
+
+    def bf16_step():
+        n = m.moe_rmsnorm(d["x"], weight, 1e-6)
+        _, st = m.moe_layer_forward(d["logits"], n["y"], *args, save_for_backward=True, workspace=ws16)
+        g = m.moe_grouped_mlp_backward(d["dout"], st, d["w_gate_up"], d["w_down"], ws16)
+        m.moe_rmsnorm_backward(g["dx"], n["sum"], weight, n["rstd"], dsum=d["dout"])
+        return [st[k] for k in ("x_perm", "gu", "h", "y_perm")]
+
+    def ckpt_step():
+        n = m.moe_rmsnorm(d["x"], weight, 1e-6, quantize=True)
+        _, st = m.moe_layer_forward_ckpt(d["logits"], n["y"], *args, x8=(n["y_q"], n["y_scale"]), workspace=ws8)
+        g = m.moe_grouped_mlp_backward_ckpt(d["dout"], st, d["w_gate_up"], d["w_down"], ws8)
+        m.moe_rmsnorm_backward(g["dx"], n["sum"], weight, n["rstd"], dsum=d["dout"])
+        return [st[k] for k in ("x_q", "x_scale", "gu_q", "gu_scale")]
+
+    ws16 = m.LayerWorkspace(w.T, w.H, w.I, w.E, w.k, backward=True)
+    ws8 = m.LayerWorkspace(w.T, w.H, w.I, w.E, w.k, backward=True, ckpt=True)
+    res = {"workload": "qwen3_30b_a3b norm + fwd + bwd (T=4096), L2 flushed before each step"}
+    for name, step in (("state_bf16", bf16_step), ("state_8bit", ckpt_step)):
+        times = []
+        for it in range(13):
+            flush.sum()
+            torch.cuda._sleep(200000)   # the GPU is busy while the calls are issued: device time only
+            s, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            s.record()
+            kept = step()
+            e.record()
+            torch.cuda.synchronize()
+            if it >= 3:
+                times.append(s.elapsed_time(e))
+        ms = statistics.median(times)
+        res[name] = {"ms_per_step": ms, "tokens_per_s": w.T / (ms / 1e3),
+                     "state_bytes": sum(t.numel() * t.element_size() for t in kept)}
+    if m.moe_get_device_status() != 0:
+        raise RuntimeError("device status after the saved-state comparison")
+    return res
 
 
 def scaled_compare(m):

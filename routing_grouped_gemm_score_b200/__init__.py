@@ -703,30 +703,36 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Opt
     _need_shape(weight, torch.bfloat16, (H,), "weight")
     if residual is not None:
         _need_shape(residual, torch.bfloat16, (T, H), "residual")
-    want = {"y": (torch.bfloat16, (T, H)), "rstd": (torch.float32, (T,))}
-    if residual is not None:
-        want["sum"] = (torch.bfloat16, (T, H))
-    if quantize:
-        want["y_q"] = (torch.uint8, (T, H))
-        want["y_scale"] = (torch.uint8, (T, -(-H // ROWS8_BLOCK)))
+    S = -(-H // ROWS8_BLOCK)
     r = dict(out) if out else {}
-    for name, t in r.items():
-        if name not in want:
-            raise ValueError(f"out: this call does not write {name!r}")
-        if t is not None:
-            _need_shape(t, *want[name], name)
+    if r:
+        want = {"y": (torch.bfloat16, (T, H)), "rstd": (torch.float32, (T,))}
+        if residual is not None:
+            want["sum"] = (torch.bfloat16, (T, H))
+        if quantize:
+            want["y_q"], want["y_scale"] = (torch.uint8, (T, H)), (torch.uint8, (T, S))
+        for name, t in r.items():
+            if name not in want:
+                raise ValueError(f"out: this call does not write {name!r}")
+            if t is not None:
+                _need_shape(t, *want[name], name)
     context, stream = _on_device(x, weight, residual, *r.values())
     with context:
-        for name, (dtype, shape) in want.items():
-            if name not in r:
-                r[name] = torch.empty_like(x, dtype=dtype) if len(shape) == 2 and shape[1] == H else x.new_empty(
-                    shape, dtype=dtype)
-        g = r.get
-        _check(lib().moe_rmsnorm(x.data_ptr(), _ptr(residual), weight.data_ptr(), T, H, eps, _ptr(g("sum")),
-                                 _ptr(r["y"]), _ptr(g("y_q")), _ptr(g("y_scale")), _ptr(r["rstd"]), stream),
-               "moe_rmsnorm")
-    if residual is None:
-        r["sum"] = x
+        y = r["y"] if "y" in r else torch.empty_like(x)
+        rstd = r["rstd"] if "rstd" in r else x.new_empty((T,), dtype=torch.float32)
+        s = x   # without a residual nothing is stored
+        if residual is not None:
+            s = r["sum"] if "sum" in r else torch.empty_like(x)
+        q = scale = None
+        if quantize:
+            q = r["y_q"] if "y_q" in r else torch.empty_like(x, dtype=torch.uint8)
+            scale = r["y_scale"] if "y_scale" in r else x.new_empty((T, S), dtype=torch.uint8)
+        _check(lib().moe_rmsnorm(x.data_ptr(), _ptr(residual), weight.data_ptr(), T, H, eps,
+                                 None if residual is None else _ptr(s), _ptr(y), _ptr(q), _ptr(scale), _ptr(rstd),
+                                 stream), "moe_rmsnorm")
+    r = {"y": y, "sum": s, "rstd": rstd}
+    if quantize:
+        r["y_q"], r["y_scale"] = q, scale
     return r
 
 

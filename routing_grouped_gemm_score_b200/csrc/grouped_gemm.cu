@@ -2198,22 +2198,13 @@ bool make_map_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class K>
-cudaError_t set_smem_once(K kern, size_t bytes, std::once_flag& once, cudaError_t& status) {
-    std::call_once(once, [&] {
-        status = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    });
-    return status;
-}
-
 template <int EPI, bool B_MN>
 cudaError_t launch_pair(const CUtensorMap& a, const CUtensorMap& a64, const CUtensorMap& b, const Params& p,
                         int64_t max_tiles, cudaStream_t st, const CUtensorMap* c = nullptr,
                         const CUtensorMap* c2 = nullptr) {
     auto kern = gemm_pair_kernel<EPI, B_MN>;
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    if (set_smem_once(kern, kSmemPBytes, once, attr) != cudaSuccess) return attr;
+    static PerDeviceFlag configured;
+    if (const cudaError_t e = allow_smem(kern, kSmemPBytes, configured); e != cudaSuccess) return e;
     if (max_tiles <= 0) return cudaSuccess;
     int64_t clusters = sm_count() / 2;
     if (clusters > max_tiles) clusters = max_tiles;
@@ -2244,9 +2235,8 @@ cudaError_t launch_1cta(const CUtensorMap& a, const CUtensorMap& b, const Params
                         int64_t max_tiles, cudaStream_t st, const CUtensorMap* c = nullptr,
                         const CUtensorMap* c2 = nullptr) {
     auto kern = gemm_1cta_kernel<EPI, A_MN, B_MN, GROUP_K>;
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    if (set_smem_once(kern, kSmem1Bytes, once, attr) != cudaSuccess) return attr;
+    static PerDeviceFlag configured;
+    if (const cudaError_t e = allow_smem(kern, kSmem1Bytes, configured); e != cudaSuccess) return e;
     if (max_tiles <= 0) return cudaSuccess;
     int64_t grid = sm_count();
     if (grid > max_tiles) grid = max_tiles;
@@ -2333,9 +2323,8 @@ cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t max_tiles, int threa
 
 cudaError_t launch_wgrad_pair(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const Params& p,
                               int64_t max_tiles, cudaStream_t st) {
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    if (set_smem_once(gemm_wgrad_pair_kernel, kSmemWBytes, once, attr) != cudaSuccess) return attr;
+    static PerDeviceFlag configured;
+    if (const cudaError_t e = allow_smem(gemm_wgrad_pair_kernel, kSmemWBytes, configured); e != cudaSuccess) return e;
     if (max_tiles <= 0) return cudaSuccess;
     return launch_clusters(gemm_wgrad_pair_kernel, max_tiles, kThreads, kSmemWBytes, st, a, b, c, p);
 }
@@ -2344,9 +2333,8 @@ template <int NR>
 cudaError_t launch_mlp(const CUtensorMap& x_rows, const CUtensorMap& w_gate_up, const CUtensorMap& h_rows,
                        const CUtensorMap& w_down, const Params& p, int64_t grid, cudaStream_t st) {
     auto kern = gemm_swap_mlp_kernel<NR>;
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    if (set_smem_once(kern, swap_smem_bytes<NR>(), once, attr) != cudaSuccess) return attr;
+    static PerDeviceFlag configured;
+    if (const cudaError_t e = allow_smem(kern, swap_smem_bytes<NR>(), configured); e != cudaSuccess) return e;
     return launch_chained(kern, dim3((unsigned)grid), dim3(kThreads), swap_smem_bytes<NR>(), st, x_rows, w_gate_up,
                           h_rows, w_down, p);
 }
@@ -2354,9 +2342,8 @@ cudaError_t launch_mlp(const CUtensorMap& x_rows, const CUtensorMap& w_gate_up, 
 template <int EPI, int NR>
 cudaError_t launch_swap(const CUtensorMap& x_rows, const CUtensorMap& w, const Params& p, cudaStream_t st) {
     auto kern = gemm_swap_kernel<EPI, NR>;
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    if (set_smem_once(kern, swap_smem_bytes<NR>(), once, attr) != cudaSuccess) return attr;
+    static PerDeviceFlag configured;
+    if (const cudaError_t e = allow_smem(kern, swap_smem_bytes<NR>(), configured); e != cudaSuccess) return e;
     // upper bound of the tiles without reading the device counts
     const int64_t bound = ((int64_t)p.rows / NR + p.groups) * (int64_t)p.n_blocks;
     if (bound <= 0) return cudaSuccess;

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/moe_b200.h"
 
 namespace moe {
@@ -44,6 +46,23 @@ cudaError_t launch_chained(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+}
+
+// Allows a kernel `bytes` of dynamic shared memory, once per device (the setting
+// belongs to the current device); a failure is tried again on the next call.
+struct PerDeviceFlag {
+    std::atomic<bool> done[64] = {};
+};
+template <class K>
+cudaError_t allow_smem(K kern, size_t bytes, PerDeviceFlag& flag) {
+    int device = 0;
+    const cudaError_t got = cudaGetDevice(&device);
+    if (got != cudaSuccess) return got;
+    const bool known = device >= 0 && device < 64;
+    if (known && flag.done[device].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && known) flag.done[device].store(true, std::memory_order_release);
+    return e;
 }
 
 // Tokens handled by one block of the router / rank kernels (a power of two,

@@ -348,9 +348,8 @@ cudaError_t launch_bwd(const bf16* dy, const bf16* s, const bf16* weight, const 
                        int H, bf16* dx, float* partial, int64_t blocks, const BwdShape& b, cudaStream_t st,
                        unsigned* err) {
     auto kern = rmsnorm_backward_kernel<CH>;
-    // per device, so set on every call (a host-side table write)
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBwdSmem);
-    if (e != cudaSuccess) return e;
+    static PerDeviceFlag configured;
+    if (const cudaError_t e = allow_smem(kern, kBwdSmem, configured); e != cudaSuccess) return e;
     kern<<<(unsigned)blocks, row_threads(H, CH), b.smem, st>>>(dy, s, reinterpret_cast<const uint4*>(weight), rstd, dsum,
                                                                T, H, reinterpret_cast<uint4*>(dx), partial, b.stages, err);
     return cudaGetLastError();
