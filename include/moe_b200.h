@@ -571,7 +571,8 @@ moe_status moe_grouped_mlp_backward_ckpt(const moe_bf16* dout, int64_t T, int H,
  * tests compare them bit for bit, or against the oracle) and differ only in
  * speed; by default (MOE_TESTING_AUTO everywhere) the library chooses by the
  * shapes alone.
- *  gemm_tiles    group-M GEMMs on single-CTA 128-row tiles or CTA-pair tiles;
+ *  gemm_tiles    group-M GEMMs (and the weight gradients of
+ *                moe_grouped_mlp_backward_ckpt) on single-CTA or CTA-pair tiles;
  *                or the forward GEMMs on swap-AB tiles (weights as the 128-row
  *                operand, 64 token rows per tile; the backward GEMMs then take
  *                single-CTA tiles); SWAP_UNFUSED: swap-AB tiles with the

@@ -1375,7 +1375,11 @@ __global__ void __launch_bounds__(GROUP_K ? kThreadsK : kThreads, 1)
 // barrier. Without the padding, each expert's last slice had to pass through a
 // warp per CTA that zeroed the rows past its end and released them to the
 // leader: about 1 us a tile, 274 against 262 us of the single-CTA kernel for the
-// Qwen3-30B-A3B gate_up gradient.
+// Qwen3-30B-A3B gate_up gradient (231 padded; Llama-4: 1168 against 1302).
+// What bounds it (timed in parts, Qwen3-30B-A3B): loads alone take 147 us, MMAs alone
+// 169, the epilogue with its stores 147; nothing is saturated (ncu: DRAM 51 %,
+// tensor pipe 40 %, L2 reads 30 %), so the rest is the latency between the roles
+// on tiles of four K slices.
 // Shared memory of gemm_wgrad_pair_kernel: a ring of 5 stages, and two store
 // buffers of 32 rows x 64 columns per epilogue warp, so that a tile's stores have
 // the whole next tile to be read out. (With one buffer of 32 x 32 the epilogue
@@ -2198,6 +2202,30 @@ bool make_map_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Launches a kernel of CTA pairs (clusters of two), chained as launch_chained.
+template <class... KArgs, class... Args>
+cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t max_tiles, int threads, size_t smem, cudaStream_t st,
+                            Args&&... args) {
+    int64_t clusters = sm_count() / 2;
+    if (clusters > max_tiles) clusters = max_tiles;
+    if (clusters < 1) clusters = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * clusters));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeClusterDimension;
+    attrs[0].val.clusterDim.x = 2;
+    attrs[0].val.clusterDim.y = 1;
+    attrs[0].val.clusterDim.z = 1;
+    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[1].val.programmaticStreamSerializationAllowed = chained_launches() ? 1 : 0;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+}
+
 template <int EPI, bool B_MN>
 cudaError_t launch_pair(const CUtensorMap& a, const CUtensorMap& a64, const CUtensorMap& b, const Params& p,
                         int64_t max_tiles, cudaStream_t st, const CUtensorMap* c = nullptr,
@@ -2206,28 +2234,11 @@ cudaError_t launch_pair(const CUtensorMap& a, const CUtensorMap& a64, const CUte
     static PerDeviceFlag configured;
     if (const cudaError_t e = allow_smem(kern, kSmemPBytes, configured); e != cudaSuccess) return e;
     if (max_tiles <= 0) return cudaSuccess;
-    int64_t clusters = sm_count() / 2;
-    if (clusters > max_tiles) clusters = max_tiles;
-    if (clusters < 1) clusters = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * clusters));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemPBytes;
-    cfg.stream = st;
-    cudaLaunchAttribute attrs[2];
-    attrs[0].id = cudaLaunchAttributeClusterDimension;
-    attrs[0].val.clusterDim.x = 2;
-    attrs[0].val.clusterDim.y = 1;
-    attrs[0].val.clusterDim.z = 1;
-    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see launch_chained
-    attrs[1].val.programmaticStreamSerializationAllowed = chained_launches() ? 1 : 0;
-    cfg.attrs = attrs;
-    cfg.numAttrs = 2;
     CUtensorMap unused{};   // read only when q.tma_out / q.tma_out2 say so
     Params q = p;
     q.tma_out = c != nullptr;
     q.tma_out2 = c2 != nullptr;
-    return cudaLaunchKernelEx(&cfg, kern, a, a64, b, c ? *c : unused, c2 ? *c2 : unused, q);
+    return launch_clusters(kern, max_tiles, kThreads, kSmemPBytes, st, a, a64, b, c ? *c : unused, c2 ? *c2 : unused, q);
 }
 
 template <int EPI, bool A_MN, bool B_MN, bool GROUP_K>
@@ -2297,28 +2308,16 @@ bool use_swap_tiles(int64_t rows, int groups) {
     return rows <= (int64_t)groups * 16;
 }
 
-// Launches a kernel of CTA pairs (clusters of two), chained as launch_chained.
-template <class... KArgs, class... Args>
-cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t max_tiles, int threads, size_t smem, cudaStream_t st,
-                            Args&&... args) {
-    int64_t clusters = sm_count() / 2;
-    if (clusters > max_tiles) clusters = max_tiles;
-    if (clusters < 1) clusters = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * clusters));
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attrs[2];
-    attrs[0].id = cudaLaunchAttributeClusterDimension;
-    attrs[0].val.clusterDim.x = 2;
-    attrs[0].val.clusterDim.y = 1;
-    attrs[0].val.clusterDim.z = 1;
-    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[1].val.programmaticStreamSerializationAllowed = chained_launches() ? 1 : 0;
-    cfg.attrs = attrs;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+// Weight gradients on CTA pairs (row blocks padded to 16): for more output rows than
+// one CTA's 128, and from 128 rows per expert on. Measured, pair against single
+// tiles, dW_down + dW_gate_up: Qwen3-30B-A3B widths, 32 rows per expert 104 + 182
+// against 96 + 163 us, 128 rows 92 + 171 against 97 + 181, 256 rows 125 + 231
+// against 136 + 251; Mixtral widths, 16 rows 204 + 370 against 175 + 328, 128 rows
+// 363 + 414 against 368 + 430. With few K slices a tile is all hand-over.
+bool use_pair_wgrad(int64_t rows, int groups, int M) {
+    const int forced = kernel_override().gemm_tiles;
+    if (forced != MOE_TESTING_AUTO) return forced == MOE_TESTING_GEMM_PAIR;
+    return M > BM1 && rows >= (int64_t)groups * 128;
 }
 
 cudaError_t launch_wgrad_pair(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const Params& p,
@@ -2664,7 +2663,7 @@ cudaError_t gemm_wgrad(const bf16* X, const bf16* D, int64_t rows, const int32_t
     Params p = base_params(E, rows, offsets, err);
     p.M = M;
     p.N = N;
-    const bool pair = blocks16 && M > BM1;
+    const bool pair = blocks16 && use_pair_wgrad(rows, E, M);
     const int m_tile = pair ? BMP : BM1;
     p.m_blocks = (M + m_tile - 1) / m_tile;
     p.n_blocks = (N + BN - 1) / BN;

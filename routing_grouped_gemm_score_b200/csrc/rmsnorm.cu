@@ -9,8 +9,11 @@
 // Backward, with xhat = s rstd:
 //   dx_i = rstd (w_i dy_i - xhat_i c) (+ dsum_i),  c = sum_j w_j dy_j xhat_j / H
 //   dw_i = sum_t dy_{t,i} xhat_{t,i}
-// Sums run in fp32 in a fixed order. Both are bound by HBM bandwidth: the row
-// stays in registers between its one read and its one write.
+// Sums run in fp32 in a fixed order. Both are bound by HBM bandwidth: a row is
+// read once, stays in registers (forward) or in shared memory (backward) until its
+// sum is known, and is written once. Measured: 16384 rows of 5120 with a residual
+// and both outputs 122 us (6.2 TB/s), their backward for 8192 rows 59 + 5 us for
+// dweight (5.7 TB/s); one row of 2048 2.2 us.
 #include "moe_internal.h"
 #include "rows8.cuh"
 
@@ -49,14 +52,13 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Forward. One row per block, whose threads hold CH 8-column chunks each. The
-// pointers may alias as documented (sum with
-// x or residual): a row's elements are read before they are written, by the
-// same thread, so no pointer is marked restrict or read through the
-// non-coherent path.
+// pointers may alias as documented (sum with x or residual, y with x): a row's
+// elements are read before they are written, by the same thread, so no pointer is
+// marked restrict or read through the non-coherent path.
 template <int CH>
 __global__ void __launch_bounds__(32 * kMaxWarps)
-    rmsnorm_kernel(const uint4* x, const uint4* residual, const uint4* weight, int H, float eps,
-                               uint4* sum, uint4* y, uint8_t* y_q, uint8_t* y_scale, float* rstd_out) {
+    rmsnorm_kernel(const uint4* x, const uint4* residual, const uint4* weight, int H, float eps, uint4* sum, uint4* y,
+                   uint8_t* y_q, uint8_t* y_scale, float* rstd_out) {
     __shared__ float red[kMaxWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int width = (int)blockDim.x, me = (int)threadIdx.x;

@@ -87,7 +87,8 @@ def backward(d, st, **kw):
 # T, H, I, E, k: one token; one expert; widths that end inside a block of 32 and
 # inside a tile; experts without rows; each kernel family by its own rule
 SHAPES = [(1, 8, 8, 1, 1), (1, 64, 72, 5, 3), (61, 128, 256, 8, 2), (40, 200, 40, 16, 4), (64, 264, 104, 4, 4),
-          (300, 128, 328, 3, 2), (1500, 96, 64, 2, 1), (257, 512, 24, 1, 1), (130, 64, 520, 12, 12)]
+          (300, 128, 328, 3, 2), (1500, 96, 64, 2, 1), (257, 512, 24, 1, 1), (130, 64, 520, 12, 12),
+          (700, 264, 200, 3, 2)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k", SHAPES)
