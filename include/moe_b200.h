@@ -541,8 +541,8 @@ moe_status moe_layer_forward_ckpt(const float* logits, const moe_bf16* x, int64_
  * (the same gradients: the weight p is applied to the activation's side, so dout
  * enters the products unrounded and y_perm is not needed). Accumulation is fp32;
  * p a, [dg | du] and each row's dx are rounded to bf16, the tensor cores' operand
- * type. dprob sums 64-column groups in column order, then the groups in order,
- * so it is the same on every run. An expert with no rows gets zero weight
+ * type. dprob sums 64-column groups in column order, then the groups in a fixed
+ * order, so it is the same on every run. An expert with no rows gets zero weight
  * gradients; T = 0 gives zero weight gradients.
  * The stages recorded by moe_trace_set are:
  *   [0] start  [1] dout by row  [2] down dgrad + SwiGLU backward  [3] down wgrad

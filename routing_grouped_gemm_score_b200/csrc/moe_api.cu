@@ -882,7 +882,7 @@ moe_status moe_grouped_mlp_backward_ckpt(const moe_bf16* dout, int64_t T, int H,
     if (e == cudaSuccess)
         e = gemm_down_dgrad_swiglu8(L.rows, L.R, blocks, E, H, I, B(w_down), gu8, A, offsets, L.prob_row, L.dgu, L.h,
                                     L.row_dot, st, err);
-    if (e == cudaSuccess) e = launch_row_dot_sum(L.row_dot, (I + 63) / 64, L.pad_row, A, L.R, dprob, st, err);
+    if (e == cudaSuccess) e = launch_row_dot_sum(L.row_dot, (I + 63) / 64, L.pad_row, A, L.R, dprob, st, err, false);
     if (e == cudaSuccess) e = trace_mark(2, st);
     if (e == cudaSuccess)
         e = gemm_wgrad(L.h, L.rows, L.R, blocks, E, I, H, reinterpret_cast<bf16*>(dw_down), st, err, true);

@@ -150,9 +150,10 @@ cudaError_t launch_combine_backward(const bf16* dout, const bf16* y_perm, const 
 // dy[r] = dout[sorted_token[r]] for r < offsets[E] (-1: a zero row).
 cudaError_t launch_gather_rows(const bf16* dout, const int32_t* sorted_token, int64_t T, const int32_t* offsets,
                                int E, int64_t A, int H, bf16* dy, cudaStream_t st, unsigned* err);
-// dprob[i] = sum_{q < nq} row_dot[row_of[i] * nq + q], q ascending.
+// dprob[i] = sum_{q < nq} row_dot[row_of[i] * nq + q], in_order: q ascending, else
+// in another fixed order.
 cudaError_t launch_row_dot_sum(const float* row_dot, int nq, const int32_t* row_of, int64_t n, int64_t A,
-                               float* dprob, cudaStream_t st, unsigned* err);
+                               float* dprob, cudaStream_t st, unsigned* err, bool in_order = true);
 
 // Values in the 8-bit row format and their scale bytes (rows8.cuh, rows8.cu).
 // Rows of parts * cols columns (parts 1 or 2, each with its own blocks); scales

@@ -18,6 +18,8 @@ constexpr int kThreads = 256;
 constexpr int kMaxExperts = 256;
 constexpr int kChunks = 4;                   // 8-column chunks of a lane in one unit
 constexpr int kUnitChunks = 32 * kChunks;    // chunks of a unit (blocks of four chunks, padded)
+constexpr int kSpreadChunks = 2;             // the same for the dispatches
+constexpr int kSpreadUnit = 32 * kSpreadChunks;
 
 // Quotient and remainder of a unit index by the units of a row.
 __device__ __forceinline__ void split_unit(int64_t u, int per_row, int64_t& row, int& part) {
@@ -160,7 +162,8 @@ __device__ __forceinline__ void zero_pad_rows(const int* off, const int* pad, in
 
 // One token's row to the k rows that its assignments hold: bf16 as it is (Q8
 // false) or read back from 8 bits (Q8 true). Each token's row is read once. A
-// warp owns a unit of one token's row; lane j holds the row of assignment j.
+// warp owns a unit of one token's row (512 columns: with 1024, 8192 rows of 5120
+// from 8 bits took 34 us against 27); lane j holds the row of assignment j.
 // Q8 false finds the padded rows: the expert of row_of[t, j] by bisection of the
 // blocks' offsets, then its place in the padded block. The unit of a token's
 // first columns writes pad_row and prob_row, and the first block pad_offsets. A
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(kThreads)
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int chunks = H / 8, S = rows8_blocks(H);
-    const int per_row = (chunks + kUnitChunks - 1) / kUnitChunks;
+    const int per_row = (chunks + kSpreadUnit - 1) / kSpreadUnit;
     const int64_t A = T * k, bound = pad16_rows(A, E);
     const int64_t units = T * per_row, nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
     pad_blocks(b, offsets, E, A);
@@ -209,10 +212,10 @@ __global__ void __launch_bounds__(kThreads)
                 }
             }
         }
-        uint4 v[kChunks];
+        uint4 v[kSpreadChunks];
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int c = part * kUnitChunks + 32 * i + lane;
+        for (int i = 0; i < kSpreadChunks; ++i) {
+            const int c = part * kSpreadUnit + 32 * i + lane;
             if (c >= chunks) continue;
             if (Q8) {
                 const uint8_t* qs = static_cast<const uint8_t*>(src) + t * H;
@@ -226,8 +229,8 @@ __global__ void __launch_bounds__(kThreads)
             if (r < 0) continue;
             uint4* dst = reinterpret_cast<uint4*>(rows) + r * chunks;
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const int c = part * kUnitChunks + 32 * i + lane;
+            for (int i = 0; i < kSpreadChunks; ++i) {
+                const int c = part * kSpreadUnit + 32 * i + lane;
                 if (c < chunks) dst[c] = v[i];
             }
         }
@@ -235,13 +238,19 @@ __global__ void __launch_bounds__(kThreads)
     zero_pad_rows(b.off, b.pad, E, chunks, bound, reinterpret_cast<uint4*>(rows), Q8 ? nullptr : prob_row);
 }
 
-// Blocks for a warp-per-unit kernel: enough warps for every unit, at most what
-// stays resident (8 blocks of 256 threads an SM).
-unsigned unit_blocks(int64_t units) {
-    const int64_t cap = (int64_t)sm_count() * 8;
+// Blocks for a warp-per-unit kernel: enough warps for every unit, at most `cap`
+// (each warp then loops).
+unsigned unit_blocks(int64_t units, int64_t cap) {
     const int64_t need = (units + kThreads / 32 - 1) / (kThreads / 32);
     return (unsigned)(need < cap ? need : cap);
 }
+
+// What stays resident, 8 blocks of 256 threads an SM; or a block for every eight
+// units. Rows of 5120 and [g | u] rows of 28672 columns (16384 and 8192 rows): to 8
+// bits 49 and 131 us resident, 52 and 150 with a block each; back 41 and 133
+// against 37 and 108.
+int64_t resident_blocks() { return (int64_t)sm_count() * 8; }
+constexpr int64_t kEveryBlock = (int64_t)1 << 30;
 
 int64_t format_units(int64_t rows, int cols, int parts) {
     return rows * ((4 * parts * rows8_blocks(cols) + kUnitChunks - 1) / kUnitChunks);
@@ -252,23 +261,23 @@ int64_t format_units(int64_t rows, int cols, int parts) {
 cudaError_t launch_quantize_rows(const bf16* x, int64_t rows, int cols, int parts, int block_major, uint8_t* q,
                                  uint8_t* scale, cudaStream_t st) {
     if (rows == 0) return cudaSuccess;
-    return launch_chained(quantize_rows_kernel, dim3(unit_blocks(format_units(rows, cols, parts))), dim3(kThreads), 0,
-                          st, x, rows, cols, parts, block_major, q, scale);
+    return launch_chained(quantize_rows_kernel, dim3(unit_blocks(format_units(rows, cols, parts), resident_blocks())),
+                          dim3(kThreads), 0, st, x, rows, cols, parts, block_major, q, scale);
 }
 
 cudaError_t launch_dequantize_rows(const uint8_t* q, const uint8_t* scale, int64_t rows, int cols, int parts,
                                    int block_major, bf16* x, cudaStream_t st) {
     if (rows == 0) return cudaSuccess;
-    return launch_chained(dequantize_rows_kernel, dim3(unit_blocks(format_units(rows, cols, parts))), dim3(kThreads),
-                          0, st, q, scale, rows, cols, parts, block_major, x);
+    return launch_chained(dequantize_rows_kernel, dim3(unit_blocks(format_units(rows, cols, parts), kEveryBlock)),
+                          dim3(kThreads), 0, st, q, scale, rows, cols, parts, block_major, x);
 }
 
 cudaError_t launch_spread_rows(const bf16* src, const int32_t* row_of, const int32_t* offsets, const float* prob,
                                int64_t T, int k, int E, int H, bf16* rows, float* prob_row, int32_t* pad_offsets,
                                int32_t* pad_row, cudaStream_t st, unsigned* err) {
     if (T == 0) return cudaSuccess;
-    const int64_t units = T * ((H / 8 + kUnitChunks - 1) / kUnitChunks);
-    return launch_chained(spread_rows_kernel<false>, dim3(unit_blocks(units)), dim3(kThreads), 0, st,
+    const int64_t units = T * ((H / 8 + kSpreadUnit - 1) / kSpreadUnit);
+    return launch_chained(spread_rows_kernel<false>, dim3(unit_blocks(units, resident_blocks())), dim3(kThreads), 0, st,
                           static_cast<const void*>(src), static_cast<const uint8_t*>(nullptr), row_of, offsets, prob,
                           T, k, E, H, rows, prob_row, pad_offsets, pad_row, err);
 }
@@ -277,8 +286,8 @@ cudaError_t launch_spread_rows8(const uint8_t* q, const uint8_t* scale, const in
                                 int E, int H, bf16* rows, const int32_t* pad_offsets, const int32_t* pad_row,
                                 cudaStream_t st) {
     if (T == 0) return cudaSuccess;
-    const int64_t units = T * ((H / 8 + kUnitChunks - 1) / kUnitChunks);
-    return launch_chained(spread_rows_kernel<true>, dim3(unit_blocks(units)), dim3(kThreads), 0, st,
+    const int64_t units = T * ((H / 8 + kSpreadUnit - 1) / kSpreadUnit);
+    return launch_chained(spread_rows_kernel<true>, dim3(unit_blocks(units, resident_blocks())), dim3(kThreads), 0, st,
                           static_cast<const void*>(q), scale, static_cast<const int32_t*>(nullptr), offsets,
                           static_cast<const float*>(nullptr), T, k, E, H, rows, static_cast<float*>(nullptr),
                           const_cast<int32_t*>(pad_offsets), const_cast<int32_t*>(pad_row),
