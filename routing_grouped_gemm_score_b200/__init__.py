@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -176,6 +177,11 @@ def _need(t: torch.Tensor, dtype, name: str) -> None:
 
 
 def _need_shape(t: torch.Tensor, dtype, shape: tuple, name: str) -> None:
+    try:   # one expression for the usual case; what is wrong is said below
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
     _need(t, dtype, name)
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -639,13 +645,14 @@ def moe_grouped_mlp_scaled_backward(dout: torch.Tensor, row_of: torch.Tensor, so
 ROWS8_BLOCK = 32   # columns that share a scale
 
 
-def _rows8_shape(q: torch.Tensor, parts: int, block_major: bool) -> tuple:
+@functools.lru_cache(maxsize=256)
+def _rows8_shape(shape: tuple, parts: int, block_major: bool) -> tuple:
     """(rows, cols of a part, shape of the scales) of rows [..., parts * cols]."""
-    if q.dim() != 2:
-        raise ValueError(f"rows must have two dimensions, got {tuple(q.shape)}")
+    if len(shape) != 2:
+        raise ValueError(f"rows must have two dimensions, got {tuple(shape)}")
     if parts not in (1, 2):
         raise ValueError(f"parts must be 1 or 2, got {parts}")
-    rows, width = q.shape
+    rows, width = shape
     if width % parts:
         raise ValueError(f"{width} columns do not divide into {parts} parts")
     cols = width // parts
@@ -658,7 +665,7 @@ def moe_quantize_rows(x: torch.Tensor, parts: int = 1, block_major: bool = False
     and a scale byte per 32 columns, [rows, blocks] or, block_major,
     [blocks, rows]."""
     _need(x, torch.bfloat16, "x")
-    rows, cols, scale_shape = _rows8_shape(x, parts, block_major)
+    rows, cols, scale_shape = _rows8_shape(x.shape, parts, block_major)
     context, stream = _on_device(x)
     with context:
         q = torch.empty_like(x, dtype=torch.uint8)
@@ -674,7 +681,7 @@ def moe_dequantize_rows(q: torch.Tensor, scale: torch.Tensor, parts: int = 1, bl
     state's [g | u]: moe_dequantize_rows(state["gu_q"], state["gu_scale"], parts=2,
     block_major=True)."""
     _need(q, torch.uint8, "q")
-    rows, cols, scale_shape = _rows8_shape(q, parts, block_major)
+    rows, cols, scale_shape = _rows8_shape(q.shape, parts, block_major)
     _need_shape(scale, torch.uint8, scale_shape, "scale")
     if out is not None:
         _need_shape(out, torch.bfloat16, q.shape, "out")
@@ -760,7 +767,7 @@ def moe_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor
             dx = torch.empty_like(dy)
         dweight = rstd.new_empty((H,)) if want_dweight else None
         if workspace is None and want_dweight:
-            workspace = _workspace(lib().moe_rmsnorm_backward_workspace_size(T, H), dy.device)
+            workspace = dy.new_empty((max(lib().moe_rmsnorm_backward_workspace_size(T, H), 1),), dtype=torch.uint8)
         _check(lib().moe_rmsnorm_backward(dy.data_ptr(), s.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _ptr(dsum),
                                           T, H, dx.data_ptr(), _ptr(dweight), _ptr(workspace),
                                           0 if workspace is None else workspace.numel(), stream),
@@ -769,6 +776,13 @@ def moe_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor
 
 
 # --------------------------------------------------- training state in 8 bits
+@functools.lru_cache(maxsize=256)
+def _ckpt_workspace_bytes(T: int, H: int, I: int, E: int, k: int, has_shared: int) -> tuple:
+    """Workspace bytes of the 8-bit layer's forward and backward (at least 1)."""
+    return (max(lib().moe_layer_forward_workspace_size(T, H, I, E, k, has_shared), 1),
+            max(lib().moe_grouped_mlp_backward_ckpt_workspace_size(T, H, I, E, k), 1))
+
+
 def _layer_shapes(w_gate_up: torch.Tensor, w_down: torch.Tensor, H: int) -> tuple:
     """(E, I) of a layer's expert weights, their shapes checked against H."""
     _need(w_gate_up, torch.bfloat16, "w_gate_up")
@@ -781,8 +795,10 @@ def _layer_shapes(w_gate_up: torch.Tensor, w_down: torch.Tensor, H: int) -> tupl
     return E, I
 
 
+@functools.lru_cache(maxsize=256)
 def _ckpt_spec(T: int, H: int, I: int, E: int, k: int) -> dict:
-    """Types and shapes of the 8-bit layer state."""
+    """Types and shapes of the 8-bit layer state (not to be changed: one dict per
+    shape, kept because building it takes longer than a launch)."""
     A, block = T * k, ROWS8_BLOCK
     return {
         "topk_idx": (torch.int32, (T, k)), "topk_prob": (torch.float32, (T, k)), "counts": (torch.int32, (E,)),
@@ -824,32 +840,39 @@ def moe_layer_forward_ckpt(logits: torch.Tensor, x: torch.Tensor, w_gate_up: tor
     if opts.expert_bias is not None:
         _need_shape(opts.expert_bias, torch.float32, (E,), "expert_bias")
     spec = _ckpt_spec(T, H, I, E, k)
-    st = dict(state or {})
+    st = dict(state) if state else {}
     if x8 is not None:
         st["x_q"], st["x_scale"] = x8
+    given = []
     for name, t in st.items():
         if name in spec:
-            _need_shape(t, spec[name][0], spec[name][1], name)
+            _need_shape(t, *spec[name], name)
+            given.append(t)
     if out is not None:
         _need_shape(out, torch.bfloat16, (T, H), "out")
-    context, stream = _on_device(logits, x, w_gate_up, w_down, shared_gate_up, shared_down, out, opts.expert_bias,
-                                 *[st[n] for n in spec if n in st], None if workspace is None else workspace.fwd)
+    ws = None if workspace is None else workspace.fwd
+    context, stream = _on_device(logits, x, w_gate_up, w_down, shared_gate_up, shared_down, out, opts.expert_bias, ws,
+                                 *given)
     with context:
         if out is None:
             out = torch.empty_like(x)
         for name, (dtype, shape) in spec.items():
             if name not in st:
                 st[name] = x.new_empty(shape, dtype=dtype)
-        if workspace is None:
-            workspace = LayerWorkspace(T, H, I, E, k, shared_gate_up is not None, device=x.device)
+        if ws is None:
+            ws = x.new_empty((_ckpt_workspace_bytes(T, H, I, E, k, int(shared_gate_up is not None))[0],),
+                             dtype=torch.uint8)
         oc = opts.c()
         _check(lib().moe_layer_forward_ckpt(
             _ptr(logits), _ptr(x), T, H, I, E, k, ctypes.byref(oc), _ptr(w_gate_up), _ptr(w_down),
             _ptr(shared_gate_up), _ptr(shared_down), _ptr(out), _ptr(st["topk_idx"]), _ptr(st["topk_prob"]),
             _ptr(st["counts"]), _ptr(st["offsets"]), _ptr(st["row_of"]), _ptr(st["x_q"]), _ptr(st["x_scale"]),
-            int(x8 is not None), _ptr(st["gu_q"]), _ptr(st["gu_scale"]), _ptr(workspace.fwd), workspace.fwd.numel(),
-            stream), "moe_layer_forward_ckpt")
+            int(x8 is not None), _ptr(st["gu_q"]), _ptr(st["gu_scale"]), ws.data_ptr(), ws.numel(), stream),
+            "moe_layer_forward_ckpt")
     return out, st
+
+
+_CKPT_READ = ("row_of", "topk_prob", "offsets", "x_q", "x_scale", "gu_q", "gu_scale")   # what the backward reads
 
 
 def moe_grouped_mlp_backward_ckpt(dout: torch.Tensor, state: dict, w_gate_up: torch.Tensor, w_down: torch.Tensor,
@@ -866,23 +889,23 @@ def moe_grouped_mlp_backward_ckpt(dout: torch.Tensor, state: dict, w_gate_up: to
         raise ValueError(f"row_of must be [T, k], got {tuple(s['row_of'].shape)}")
     k = s["row_of"].shape[1]
     spec = _ckpt_spec(T, H, I, E, k)
-    used = ("row_of", "topk_prob", "offsets", "x_q", "x_scale", "gu_q", "gu_scale")
-    for name in used:
-        _need_shape(s[name], spec[name][0], spec[name][1], name)
-    want = {"dx": (torch.bfloat16, (T, H)), "dw_gate_up": (torch.bfloat16, (E, H, 2 * I)),
-            "dw_down": (torch.bfloat16, (E, I, H)), "dprob": (torch.float32, (T, k))}
-    g = dict(grads or {})
-    for name, (dtype, shape) in want.items():
-        if name in g:
-            _need_shape(g[name], dtype, shape, name)
+    used = [s[name] for name in _CKPT_READ]
+    for name, t in zip(_CKPT_READ, used):
+        _need_shape(t, *spec[name], name)
+    like = {"dx": dout, "dw_gate_up": w_gate_up, "dw_down": w_down, "dprob": s["topk_prob"]}   # types and shapes
+    g = dict(grads) if grads else {}
+    for name, t in g.items():
+        if name in like:
+            _need_shape(t, like[name].dtype, like[name].shape, name)
+            used.append(t)
     ws = None if workspace is None else workspace.bwd8
-    context, stream = _on_device(dout, w_gate_up, w_down, ws, *[s[n] for n in used], *[g[n] for n in want if n in g])
+    context, stream = _on_device(dout, w_gate_up, w_down, ws, *used)
     with context:
-        for name, (dtype, shape) in want.items():
+        for name, t in like.items():
             if name not in g:
-                g[name] = dout.new_empty(shape, dtype=dtype)
+                g[name] = torch.empty_like(t)
         if ws is None:
-            ws = _workspace(lib().moe_grouped_mlp_backward_ckpt_workspace_size(T, H, I, E, k), dout.device)
+            ws = dout.new_empty((_ckpt_workspace_bytes(T, H, I, E, k, 0)[1],), dtype=torch.uint8)
         _check(lib().moe_grouped_mlp_backward_ckpt(
             _ptr(dout), T, H, I, E, k, _ptr(w_gate_up), _ptr(w_down), _ptr(s["row_of"]), _ptr(s["topk_prob"]),
             _ptr(s["offsets"]), _ptr(s["x_q"]), _ptr(s["x_scale"]), _ptr(s["gu_q"]), _ptr(s["gu_scale"]),
