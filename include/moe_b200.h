@@ -520,7 +520,7 @@ moe_status moe_grouped_mlp_scaled_backward(const moe_bf16* dout, int64_t T, int 
  *  x_q       out uint8 [T, H], x_scale out uint8 [T, ceil(H / 32)]
  *  gu_q      out uint8 [A, 2I]: two parts of I columns
  *  gu_scale  out uint8 [2 ceil(I / 32), A]: block-major
- * Other arguments, limits, traced stages (x's quantisation counts to the first)
+ * Other arguments, limits, traced stages (x's quantisation counts to the permute)
  * and the workspace (moe_layer_forward_workspace_size) as in moe_layer_forward. */
 moe_status moe_layer_forward_ckpt(const float* logits, const moe_bf16* x, int64_t T, int H, int I,
                                    int E, int k, const moe_router_opts* opts,

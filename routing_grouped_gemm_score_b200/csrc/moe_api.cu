@@ -636,7 +636,6 @@ moe_status layer_forward(const float* logits, const moe_bf16* x, int64_t T, int 
     const int n_zero = fused_mlp ? E + 1 : 0;
 
     cudaError_t e = trace_mark(0, st);
-    if (e == cudaSuccess && keep.x8.q) e = launch_quantize_rows(xb, T, H, 1, 0, keep.x8.q, keep.x8.scale, st);
     bool scanned = false, permuted = false;
     // one token block (T <= 8): the router also writes the counts and offsets
     // (no scan launch), and for at most 64 KB of rows the permuted rows too (no
@@ -649,7 +648,12 @@ moe_status layer_forward(const float* logits, const moe_bf16* x, int64_t T, int 
     if (e == cudaSuccess) e = trace_mark(1, st);
     if (e == cudaSuccess && !permuted)
         e = launch_permute(xb, T, H, L.topk_idx, k, L.offsets, E, L.rs, gather ? nullptr : L.x_perm,
-                           L.sorted_token, L.row_of, st, err);
+                           L.sorted_token, L.row_of, st, err, 0, keep.x8);
+    // x in 8 bits comes with the permute, which has the rows in registers (Qwen3-30B-
+    // A3B: 28 us together, 26 + 8 apart; Mixtral-8x7B 23, 19 + 16); where the permute
+    // kernel moves no rows it takes a launch of its own
+    if (e == cudaSuccess && keep.x8.q && (permuted || gather))
+        e = launch_quantize_rows(xb, T, H, 1, 0, keep.x8.q, keep.x8.scale, st);
     if (e == cudaSuccess) e = trace_mark(2, st);
     if (e == cudaSuccess && fused_mlp)
         e = gemm_expert_mlp_fused(L.x_perm, A, L.offsets, E, H, I, reinterpret_cast<const bf16*>(w_gate_up),

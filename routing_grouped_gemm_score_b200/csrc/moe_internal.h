@@ -65,6 +65,14 @@ cudaError_t allow_smem(K kern, size_t bytes, PerDeviceFlag& flag) {
     return e;
 }
 
+// Values in the 8-bit row format and their scale bytes (rows8.cuh, rows8.cu).
+// Rows of parts * cols columns (parts 1 or 2, each with its own blocks); scales
+// [rows][parts * S], or [parts * S][rows] when block_major, S = ceil(cols / 32).
+struct Rows8 {
+    uint8_t* q = nullptr;
+    uint8_t* scale = nullptr;
+};
+
 // Tokens handled by one block of the router / rank kernels (a power of two,
 // 8..64). Ranks inside an expert block are counted per such token block, then
 // offset by a scan. Small batches use small token blocks so that every SM gets
@@ -132,10 +140,11 @@ cudaError_t launch_pad_fill(const int32_t* offsets, const int32_t* padded_offset
 cudaError_t launch_prob_perm(const float* topk_prob, const int32_t* row_of, int64_t n, float* prob_perm,
                              cudaStream_t st);
 // row_bound: rows of x_perm and sorted_token (<= 0: T*k, the unpadded dispatch)
+// x8: with x_perm, x also goes there in 8 bits, by token (one part, scales by row)
 cudaError_t launch_permute(const bf16* x, int64_t T, int H, const int32_t* topk_idx, int k,
                            const int32_t* offsets, int E, const RouteScratch& rs, bf16* x_perm,
                            int32_t* sorted_token, int32_t* row_of, cudaStream_t st, unsigned* err,
-                           int64_t row_bound = 0);
+                           int64_t row_bound = 0, const Rows8& x8 = Rows8());
 
 // The fixed scratch array behind moe_router_topk_noalloc (routing.cu).
 size_t router_noalloc_capacity();
@@ -155,13 +164,6 @@ cudaError_t launch_gather_rows(const bf16* dout, const int32_t* sorted_token, in
 cudaError_t launch_row_dot_sum(const float* row_dot, int nq, const int32_t* row_of, int64_t n, int64_t A,
                                float* dprob, cudaStream_t st, unsigned* err, bool in_order = true);
 
-// Values in the 8-bit row format and their scale bytes (rows8.cuh, rows8.cu).
-// Rows of parts * cols columns (parts 1 or 2, each with its own blocks); scales
-// [rows][parts * S], or [parts * S][rows] when block_major, S = ceil(cols / 32).
-struct Rows8 {
-    uint8_t* q = nullptr;
-    uint8_t* scale = nullptr;
-};
 cudaError_t launch_quantize_rows(const bf16* x, int64_t rows, int cols, int parts, int block_major, uint8_t* q,
                                  uint8_t* scale, cudaStream_t st);
 cudaError_t launch_dequantize_rows(const uint8_t* q, const uint8_t* scale, int64_t rows, int cols, int parts,

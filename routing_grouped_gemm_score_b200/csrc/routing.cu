@@ -20,9 +20,11 @@
 // permutation is the same on every run.
 #include <cstdlib>
 #include <mutex>
+#include <type_traits>
 
 #include "moe_common.cuh"
 #include "moe_internal.h"
+#include "rows8.cuh"
 
 namespace moe {
 
@@ -1028,15 +1030,36 @@ __global__ void __launch_bounds__(1024)
 // local_rank, checked against the expert's block; row_of and sorted_token are
 // written here) into shared memory. Then each thread owns one 16-byte column
 // chunk (blockDim = H/8 rounded up to a warp, H <= 4096), loads it for 4
-// tokens at once and stores each to the token's k rows.
+// tokens at once and stores each to the token's k rows. Q8: the token's row also
+// goes to x8 in 8 bits (rows8.cuh), from the same registers.
 constexpr int kPermStage = 2048;
 
+// A thread's 16-byte chunk c of token t's row (zeros where have is false) in 8
+// bits. All lanes of the warp must call it together; the warp's chunks are
+// consecutive.
+__device__ __forceinline__ void put_chunk8(const Rows8& x8, int64_t t, int H8, int c, bool have, const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 p = unpack_bf16x2(w[i]);
+        f[2 * i] = p.x;
+        f[2 * i + 1] = p.y;
+    }
+    uint2 q;
+    const uint32_t byte = rows8_quantize_quad(f, q);
+    if (!have) return;
+    reinterpret_cast<uint2*>(x8.q)[t * H8 + c] = q;
+    if ((c & 3) == 0) x8.scale[t * rows8_blocks(8 * H8) + (c >> 2)] = (uint8_t)byte;
+}
+
+template <bool Q8>
 __global__ void __launch_bounds__(512)
     permute_tokens_kernel(const uint4* __restrict__ x, int64_t T, int H8, const int32_t* __restrict__ topk_idx,
                           int k, const int32_t* __restrict__ offsets, int E, const int32_t* __restrict__ block_base,
                           int nb, int tpb, const int32_t* __restrict__ local_rank, uint4* __restrict__ x_perm,
                           int32_t* __restrict__ sorted_token, int32_t* __restrict__ row_of, int64_t A,
-                          int64_t per_block, unsigned* err) {
+                          int64_t per_block, unsigned* err, const Rows8 x8) {
     __shared__ int32_t s_row[kPermStage];
     pdl_wait();
     pdl_launch_dependents();
@@ -1064,15 +1087,21 @@ __global__ void __launch_bounds__(512)
             if (row >= 0) sorted_token[row] = (int32_t)t;
         }
         __syncthreads();
-        if (!active || x_perm == nullptr) continue;   // no x_perm: the rows only
+        if ((!Q8 && !active) || x_perm == nullptr) continue;   // no x_perm: the rows only
         for (int tt0 = 0; tt0 < ntok; tt0 += 4) {
             uint4 v[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (tt0 + u < ntok) v[u] = __ldg(x + (s0 + tt0 + u) * H8 + c);
+            for (int u = 0; u < 4; ++u) {
+                if (Q8) v[u] = make_uint4(0, 0, 0, 0);
+                if (tt0 + u < ntok && (!Q8 || active)) v[u] = __ldg(x + (s0 + tt0 + u) * H8 + c);
+            }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 if (tt0 + u >= ntok) break;
+                if (Q8) {
+                    put_chunk8(x8, s0 + tt0 + u, H8, c, active, v[u]);
+                    if (!active) continue;
+                }
                 for (int j = 0; j < k; ++j) {
                     const int32_t r = s_row[(tt0 + u) * k + j];
                     if (r >= 0) x_perm[(int64_t)r * H8 + c] = v[u];
@@ -1090,13 +1119,13 @@ __global__ void __launch_bounds__(512)
 // Expert offsets are cached in shared memory per block.
 constexpr int kPermMaxExperts = 256;   // the ABI's bound on E
 
-template <int KB, int CH>
+template <int KB, int CH, bool Q8>
 __global__ void __launch_bounds__(256)
     permute_warp_kernel(const uint4* __restrict__ x, int64_t T, int H8, const int32_t* __restrict__ topk_idx,
                         int k, const int32_t* __restrict__ offsets, int E, const int32_t* __restrict__ block_base,
                         int nb, int tpb, const int32_t* __restrict__ local_rank, uint4* __restrict__ x_perm,
                         int32_t* __restrict__ sorted_token, int32_t* __restrict__ row_of, int64_t A,
-                        unsigned* err) {
+                        unsigned* err, const Rows8 x8) {
     __shared__ int32_t s_off[kPermMaxExperts + 1];
     pdl_wait();
     pdl_launch_dependents();
@@ -1159,11 +1188,13 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int h = 0; h < CH; ++h) {
                 const int c = c0 + 32 * h + lane;
+                if (Q8) v[h] = make_uint4(0, 0, 0, 0);
                 if (c < H8) v[h] = __ldg(src + c);
             }
 #pragma unroll
             for (int h = 0; h < CH; ++h) {
                 const int c = c0 + 32 * h + lane;
+                if (Q8) put_chunk8(x8, t, H8, c, c < H8, v[h]);
                 if (c >= H8) continue;
 #pragma unroll
                 for (int j = 0; j < KB; ++j)
@@ -1441,7 +1472,7 @@ cudaError_t launch_prob_perm(const float* topk_prob, const int32_t* row_of, int6
 cudaError_t launch_permute(const bf16* x, int64_t T, int H, const int32_t* topk_idx, int k,
                            const int32_t* offsets, int E, const RouteScratch& rs, bf16* x_perm,
                            int32_t* sorted_token, int32_t* row_of, cudaStream_t st, unsigned* err,
-                           int64_t row_bound) {
+                           int64_t row_bound, const Rows8& x8) {
     const int64_t A = row_bound > 0 ? row_bound : T * k;   // rows of x_perm and sorted_token
     const int nb = (int)route_blocks(T);
     if (T == 0) return cudaSuccess;
@@ -1456,24 +1487,29 @@ cudaError_t launch_permute(const bf16* x, int64_t T, int H, const int32_t* topk_
     if (regs) {
         // without x_perm only the rows are computed: 256 threads whatever H
         const int threads = x_perm == nullptr ? 256 : (H8r + 31) / 32 * 32;
+        auto kern = x8.q != nullptr && x_perm != nullptr ? permute_tokens_kernel<true> : permute_tokens_kernel<false>;
         int per_sm = 1;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, permute_tokens_kernel, threads, 0) != cudaSuccess ||
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess ||
             per_sm < 1)
             per_sm = 1;
         const int64_t slots = (int64_t)sm_count() * per_sm;
         const int64_t per_block = (T + slots - 1) / slots;
         const int64_t blocks = (T + per_block - 1) / per_block;
-        return launch_chained(permute_tokens_kernel, dim3((unsigned)blocks), dim3(threads), 0, st,
+        return launch_chained(kern, dim3((unsigned)blocks), dim3(threads), 0, st,
                               reinterpret_cast<const uint4*>(x), T, H8r, topk_idx, k, offsets, E,
                               (const int32_t*)rs.block_base, nb, route_tokens_per_block(T),
                               (const int32_t*)rs.local_rank, reinterpret_cast<uint4*>(x_perm), sorted_token, row_of,
-                              A, per_block, err);
+                              A, per_block, err, x8);
     }
     if (E > kPermMaxExperts) return cudaErrorInvalidValue;
     constexpr int kThreadsW = 256;
-    auto kern = k <= 2 ? permute_warp_kernel<2, 4>
-              : k <= 4 ? permute_warp_kernel<4, 4>
-              : k <= 8 ? permute_warp_kernel<8, 4> : permute_warp_kernel<16, 4>;
+    const auto pick = [&](auto q8) {
+        constexpr bool Q8 = decltype(q8)::value;
+        return k <= 2 ? permute_warp_kernel<2, 4, Q8>
+             : k <= 4 ? permute_warp_kernel<4, 4, Q8>
+             : k <= 8 ? permute_warp_kernel<8, 4, Q8> : permute_warp_kernel<16, 4, Q8>;
+    };
+    auto kern = x8.q != nullptr ? pick(std::true_type()) : pick(std::false_type());
     int per_sm = 1;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreadsW, 0) != cudaSuccess || per_sm < 1)
         per_sm = 1;
@@ -1483,7 +1519,7 @@ cudaError_t launch_permute(const bf16* x, int64_t T, int H, const int32_t* topk_
     return launch_chained(kern, dim3((unsigned)blocks), dim3(kThreadsW), 0, st, reinterpret_cast<const uint4*>(x), T,
                           H8r, topk_idx, k, offsets, E, (const int32_t*)rs.block_base, nb, route_tokens_per_block(T),
                           (const int32_t*)rs.local_rank, reinterpret_cast<uint4*>(x_perm), sorted_token, row_of, A,
-                          err);
+                          err, x8);
 }
 
 // Device address of g_router_noalloc_scratch on the current device. In host

@@ -107,6 +107,22 @@ def test_forward_and_backward(T, H, I, E, k, tiles):
     check_backward(d, st, g)
 
 
+@pytest.mark.parametrize("T,H,k", [(9, 40, 2), (300, 264, 3), (70, 4096, 4), (33, 4104, 2), (5, 8192, 1), (400, 5120, 16)])
+@pytest.mark.parametrize("permute", ["auto", "warp"])
+def test_x8_from_every_permute(T, H, k, permute):
+    """x8 comes from whichever kernel moves the rows (or its own), bit for bit."""
+    require_gpu()
+    force_kernels(permute=permute)
+    d = case(T, H, 8, 16, k)
+    d["x"][T // 2, H - 3], d["x"][0, 1] = float("inf"), -3.3895e38
+    d["cuda"]["x"] = d["x"].cuda()
+    _, st = forward(d)
+    status_ok()
+    want, bytes_ = ref.quantize(d["x"].double())
+    assert torch.equal(st["x_scale"].cpu(), bytes_)
+    ref.assert_within(ref.decode(st["x_q"].cpu(), bytes_), want, torch.zeros_like(want), "x8")
+
+
 def test_folded_permute():
     require_gpu()
     d = case(300, 128, 328, 3, 2)
