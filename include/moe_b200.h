@@ -546,7 +546,7 @@ moe_status moe_layer_forward_ckpt(const float* logits, const moe_bf16* x, int64_
  * gradients; T = 0 gives zero weight gradients.
  * The stages recorded by moe_trace_set are:
  *   [0] start  [1] dout by row  [2] down dgrad + SwiGLU backward  [3] down wgrad
- *   [4] gate_up dgrad  [5] token sum of dx  [6] x by row + gate_up wgrad
+ *   [4] gate_up dgrad  [5] token sum of dx, dprob, x by row  [6] gate_up wgrad
  *  row_of, topk_prob, offsets, x_q, x_scale, gu_q, gu_scale  in, from
  *      moe_layer_forward_ckpt (x_q and x_scale possibly from moe_rmsnorm)
  *  dout in bf16 [T,H]; dx out bf16 [T,H]; dw_gate_up out bf16 [E,H,2I];

@@ -260,37 +260,27 @@ __global__ void __launch_bounds__(kWarpKernelThreads)
     }
 }
 
-// dprob[i] = sum_q row_dot[row_of[i] * nq + q]: the gradient of each routing
-// weight from the per-64-column partial sums that the SwiGLU backward epilogue
-// wrote. LANES adjacent lanes per assignment: each adds every LANES-th partial,
-// ascending, then a butterfly adds theirs; a fixed order, so the result is the
-// same on every run. With one lane the partials are added in order; eight read a
-// row's partials together (128 of them, 8192 assignments: 23 against 4.5 us).
-template <int LANES>
+// dprob[i] = sum_q row_dot[row_of[i] * nq + q], q ascending: the gradient of
+// each routing weight from the per-64-column partial sums that the ScaledSwiGLU
+// backward epilogue wrote. One thread per assignment; a fixed order, so the
+// result is the same on every run.
 __global__ void __launch_bounds__(256)
     row_dot_sum_kernel(const float* __restrict__ row_dot, int nq, const int32_t* __restrict__ row_of, int64_t n,
                        int64_t A, float* __restrict__ dprob, unsigned* err) {
     pdl_wait();
     pdl_launch_dependents();
-    const int l = threadIdx.x % LANES;
-    const int64_t step = (int64_t)gridDim.x * (blockDim.x / LANES);
-    // whole groups of 32 / LANES assignments, so that a warp's lanes stay together
-    const int64_t end = (n + 32 / LANES - 1) / (32 / LANES) * (32 / LANES);
-    for (int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LANES; i < end; i += step) {
-        int64_t r = i < n ? __ldg(row_of + i) : -1;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t r = __ldg(row_of + i);
         if (r < 0 || r >= A) {
-            if (i < n) raise_error(err, kErrDeviceCheck);
-            r = -1;
+            raise_error(err, kErrDeviceCheck);
+            dprob[i] = 0.0f;
+            continue;
         }
+        const float* src = row_dot + r * nq;
         float sum = 0.0f;
-        if (r >= 0) {
-            const float* src = row_dot + r * nq;
 #pragma unroll 8
-            for (int q = l; q < nq; q += LANES) sum += __ldg(src + q);
-        }
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        if (l == 0 && i < n) dprob[i] = sum;
+        for (int q = 0; q < nq; ++q) sum += __ldg(src + q);
+        dprob[i] = sum;
     }
 }
 
@@ -306,14 +296,13 @@ cudaError_t launch_gather_rows(const bf16* dout, const int32_t* sorted_token, in
 }
 
 cudaError_t launch_row_dot_sum(const float* row_dot, int nq, const int32_t* row_of, int64_t n, int64_t A,
-                               float* dprob, cudaStream_t st, unsigned* err, bool in_order) {
+                               float* dprob, cudaStream_t st, unsigned* err) {
     if (n == 0) return cudaSuccess;
-    auto kern = in_order ? row_dot_sum_kernel<1> : row_dot_sum_kernel<8>;
-    const int64_t per_block = in_order ? 256 : 32;
-    int64_t blocks = (n + per_block - 1) / per_block;
+    int64_t blocks = (n + 255) / 256;
     const int64_t cap = (int64_t)sm_count() * 8;
     if (blocks > cap) blocks = cap;
-    return launch_chained(kern, dim3((unsigned)blocks), dim3(256), 0, st, row_dot, nq, row_of, n, A, dprob, err);
+    return launch_chained(row_dot_sum_kernel, dim3((unsigned)blocks), dim3(256), 0, st, row_dot, nq, row_of, n, A,
+                          dprob, err);
 }
 
 cudaError_t launch_combine(const bf16* y_perm, const int32_t* row_of, const float* probs,

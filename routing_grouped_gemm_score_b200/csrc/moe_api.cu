@@ -886,7 +886,6 @@ moe_status moe_grouped_mlp_backward_ckpt(const moe_bf16* dout, int64_t T, int H,
     if (e == cudaSuccess)
         e = gemm_down_dgrad_swiglu8(L.rows, L.R, blocks, E, H, I, B(w_down), gu8, A, offsets, L.prob_row, L.dgu, L.h,
                                     L.row_dot, st, err);
-    if (e == cudaSuccess) e = launch_row_dot_sum(L.row_dot, (I + 63) / 64, L.pad_row, A, L.R, dprob, st, err, false);
     if (e == cudaSuccess) e = trace_mark(2, st);
     if (e == cudaSuccess)
         e = gemm_wgrad(L.h, L.rows, L.R, blocks, E, I, H, reinterpret_cast<bf16*>(dw_down), st, err, true);
@@ -896,10 +895,9 @@ moe_status moe_grouped_mlp_backward_ckpt(const moe_bf16* dout, int64_t T, int H,
         e = gemm_gate_up_dgrad(L.dgu, L.R, blocks, E, H, I, B(w_gate_up), L.rows, st, err);
     if (e == cudaSuccess) e = trace_mark(4, st);
     if (e == cudaSuccess)
-        e = launch_combine(L.rows, L.pad_row, nullptr, T, k, H, L.R, nullptr, reinterpret_cast<bf16*>(dx), st, err);
+        e = launch_finish_rows(Rows8{const_cast<uint8_t*>(x_q), const_cast<uint8_t*>(x_scale)}, offsets, T, k, E, H,
+                               L.rows, L.pad_row, L.row_dot, (I + 63) / 64, reinterpret_cast<bf16*>(dx), dprob, st);
     if (e == cudaSuccess) e = trace_mark(5, st);
-    if (e == cudaSuccess)
-        e = launch_spread_rows8(x_q, x_scale, offsets, T, k, E, H, L.rows, L.pad_offsets, L.pad_row, st);
     if (e == cudaSuccess)
         e = gemm_wgrad(L.rows, L.dgu, L.R, blocks, E, H, 2 * I, reinterpret_cast<bf16*>(dw_gate_up), st, err, true);
     if (e == cudaSuccess) e = trace_mark(6, st);

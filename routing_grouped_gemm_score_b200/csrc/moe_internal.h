@@ -159,10 +159,9 @@ cudaError_t launch_combine_backward(const bf16* dout, const bf16* y_perm, const 
 // dy[r] = dout[sorted_token[r]] for r < offsets[E] (-1: a zero row).
 cudaError_t launch_gather_rows(const bf16* dout, const int32_t* sorted_token, int64_t T, const int32_t* offsets,
                                int E, int64_t A, int H, bf16* dy, cudaStream_t st, unsigned* err);
-// dprob[i] = sum_{q < nq} row_dot[row_of[i] * nq + q], in_order: q ascending, else
-// in another fixed order.
+// dprob[i] = sum_{q < nq} row_dot[row_of[i] * nq + q], q ascending.
 cudaError_t launch_row_dot_sum(const float* row_dot, int nq, const int32_t* row_of, int64_t n, int64_t A,
-                               float* dprob, cudaStream_t st, unsigned* err, bool in_order = true);
+                               float* dprob, cudaStream_t st, unsigned* err);
 
 cudaError_t launch_quantize_rows(const bf16* x, int64_t rows, int cols, int parts, int block_major, uint8_t* q,
                                  uint8_t* scale, cudaStream_t st);
@@ -177,10 +176,13 @@ constexpr int64_t pad16_rows(int64_t A, int E) { return A + 15 * (A < E ? A : (i
 cudaError_t launch_spread_rows(const bf16* src, const int32_t* row_of, const int32_t* offsets, const float* prob,
                                int64_t T, int k, int E, int H, bf16* rows, float* prob_row, int32_t* pad_offsets,
                                int32_t* pad_row, cudaStream_t st, unsigned* err);
-// the same rows from src in 8 bits, with pad_offsets and pad_row given
-cudaError_t launch_spread_rows8(const uint8_t* q, const uint8_t* scale, const int32_t* offsets, int64_t T, int k,
-                                int E, int H, bf16* rows, const int32_t* pad_offsets, const int32_t* pad_row,
-                                cudaStream_t st);
+// What is left to do by token between the gate_up dgrad and its weight's gradient,
+// with pad_row given: dx[t] = sum_j rows[pad_row[t, j]] (each row's dx), then those
+// rows become x[t], read back from x8 (the padding zeros); and dprob[t, j] = the sum
+// of row_dot [row][nq] over the row.
+cudaError_t launch_finish_rows(const Rows8& x8, const int32_t* offsets, int64_t T, int k, int E, int H, bf16* rows,
+                               const int32_t* pad_row, const float* row_dot, int nq, bf16* dx, float* dprob,
+                               cudaStream_t st);
 
 // RMSNorm with the residual's addition, and its backward (rmsnorm.cu).
 constexpr int kRmsnormMaxH = 16384;

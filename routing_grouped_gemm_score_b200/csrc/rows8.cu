@@ -1,7 +1,7 @@
 // rows8.cu -- rows in the 8-bit format of rows8.cuh: to it from bf16 and back,
-// and the two dispatches of the 8-bit checkpoint's backward, which write each
-// routed row's output gradient and its x, read back from the token's 8-bit row,
-// into expert blocks padded to whole K steps of 16 rows.
+// and the two steps by token of the 8-bit checkpoint's backward: each routed row's
+// output gradient into expert blocks padded to whole K steps of 16 rows, and, once
+// those rows hold dx, their sum by token and x in their place.
 //
 // All of them are bound by HBM bandwidth. A warp owns a unit of up to 1024
 // consecutive columns of one row (32 lanes x 4 chunks of 8 columns), its loads
@@ -147,43 +147,41 @@ __device__ __forceinline__ void pad_blocks(PadBlocks& b, const int32_t* __restri
 }
 
 // Zero rows at the blocks' ends, a warp per row: rows (and prob_row, if given).
-__device__ __forceinline__ void zero_pad_rows(const int* off, const int* pad, int E, int chunks, int64_t bound,
-                                              uint4* rows, float* prob_row) {
+__device__ __forceinline__ void zero_pad_rows(const PadBlocks& b, int E, int chunks, int64_t bound, uint4* rows,
+                                              float* prob_row) {
     const int lane = threadIdx.x & 31;
     const int64_t nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
     for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; i < 16 * (int64_t)E; i += nwarps) {
         const int e = (int)(i >> 4);
-        const int64_t r = (int64_t)pad[e] + max(off[e + 1] - off[e], 0) + (i & 15);
-        if (r >= pad[e + 1] || r >= bound) continue;
+        const int64_t r = (int64_t)b.pad[e] + max(b.off[e + 1] - b.off[e], 0) + (i & 15);
+        if (r >= b.pad[e + 1] || r >= bound) continue;
         for (int c = lane; c < chunks; c += 32) rows[r * chunks + c] = make_uint4(0, 0, 0, 0);
         if (prob_row != nullptr && lane == 0) prob_row[r] = 0.0f;
     }
 }
 
-// One token's row to the k rows that its assignments hold: bf16 as it is (Q8
-// false) or read back from 8 bits (Q8 true). Each token's row is read once. A
-// warp owns a unit of one token's row (512 columns: with 1024, 8192 rows of 5120
-// from 8 bits took 34 us against 27); lane j holds the row of assignment j.
-// Q8 false finds the padded rows: the expert of row_of[t, j] by bisection of the
-// blocks' offsets, then its place in the padded block. The unit of a token's
-// first columns writes pad_row and prob_row, and the first block pad_offsets. A
-// row outside its range is recorded and skipped (pad_row -1).
-template <bool Q8>
+// One token's row to the k padded rows of its assignments. Each token's row is
+// read once. A warp owns a unit of one token's row (512 columns: with 1024, 8192
+// rows of 5120 from 8 bits took 34 us against 27); lane j finds the row of
+// assignment j: the expert of row_of[t, j] by bisection of the blocks' offsets,
+// then its place in the padded block. The unit of a token's first columns writes
+// pad_row and prob_row, and the first block pad_offsets. A row outside its range
+// is recorded and skipped (pad_row -1).
 __global__ void __launch_bounds__(kThreads)
-    spread_rows_kernel(const void* __restrict__ src, const uint8_t* __restrict__ scale,
-                       const int32_t* __restrict__ row_of, const int32_t* __restrict__ offsets,
-                       const float* __restrict__ prob, int64_t T, int k, int E, int H, bf16* __restrict__ rows,
-                       float* __restrict__ prob_row, int32_t* pad_offsets, int32_t* pad_row, unsigned* err) {
+    spread_rows_kernel(const uint4* __restrict__ src, const int32_t* __restrict__ row_of,
+                       const int32_t* __restrict__ offsets, const float* __restrict__ prob, int64_t T, int k, int E,
+                       int H, uint4* __restrict__ rows, float* __restrict__ prob_row,
+                       int32_t* __restrict__ pad_offsets, int32_t* __restrict__ pad_row, unsigned* err) {
     __shared__ PadBlocks b;
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int chunks = H / 8, S = rows8_blocks(H);
+    const int chunks = H / 8;
     const int per_row = (chunks + kSpreadUnit - 1) / kSpreadUnit;
     const int64_t A = T * k, bound = pad16_rows(A, E);
     const int64_t units = T * per_row, nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
     pad_blocks(b, offsets, E, A);
-    if (!Q8 && blockIdx.x == 0)
+    if (blockIdx.x == 0)
         for (int i = threadIdx.x; i <= E; i += kThreads) pad_offsets[i] = b.pad[i];
     for (int64_t u = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; u < units; u += nwarps) {
         int64_t t;
@@ -191,51 +189,128 @@ __global__ void __launch_bounds__(kThreads)
         split_unit(u, per_row, t, part);
         int32_t mine = -1;
         if (lane < k) {
-            if (Q8) {
-                mine = __ldg(pad_row + t * k + lane);
-            } else {
-                const int32_t row = __ldg(row_of + t * k + lane);
-                if (row >= 0 && row < A) {
-                    int lo = 0, hi = E - 1;   // last expert whose block starts at or before the row
-                    while (lo < hi) {
-                        const int mid = (lo + hi + 1) >> 1;
-                        if (b.off[mid] <= row) lo = mid;
-                        else hi = mid - 1;
-                    }
-                    const int64_t r = (int64_t)b.pad[lo] + (row - b.off[lo]);
-                    if (row >= b.off[lo] && row < b.off[lo + 1] && r < bound) mine = (int32_t)r;
+            const int32_t row = __ldg(row_of + t * k + lane);
+            if (row >= 0 && row < A) {
+                int lo = 0, hi = E - 1;   // last expert whose block starts at or before the row
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (b.off[mid] <= row) lo = mid;
+                    else hi = mid - 1;
                 }
-                if (mine < 0) raise_error(err, kErrDeviceCheck);
-                if (part == 0) {
-                    pad_row[t * k + lane] = mine;
-                    if (mine >= 0) prob_row[mine] = __ldg(prob + t * k + lane);
-                }
+                const int64_t r = (int64_t)b.pad[lo] + (row - b.off[lo]);
+                if (row >= b.off[lo] && row < b.off[lo + 1] && r < bound) mine = (int32_t)r;
+            }
+            if (mine < 0) raise_error(err, kErrDeviceCheck);
+            if (part == 0) {
+                pad_row[t * k + lane] = mine;
+                if (mine >= 0) prob_row[mine] = __ldg(prob + t * k + lane);
             }
         }
         uint4 v[kSpreadChunks];
 #pragma unroll
         for (int i = 0; i < kSpreadChunks; ++i) {
             const int c = part * kSpreadUnit + 32 * i + lane;
-            if (c >= chunks) continue;
-            if (Q8) {
-                const uint8_t* qs = static_cast<const uint8_t*>(src) + t * H;
-                v[i] = rows8_dequantize8(__ldg(reinterpret_cast<const uint2*>(qs) + c), __ldg(scale + t * S + (c >> 2)));
-            } else {
-                v[i] = __ldg(reinterpret_cast<const uint4*>(src) + t * chunks + c);
-            }
+            if (c < chunks) v[i] = __ldg(src + t * chunks + c);
         }
         for (int j = 0; j < k; ++j) {
             const int64_t r = __shfl_sync(0xFFFFFFFFu, mine, j);
             if (r < 0) continue;
-            uint4* dst = reinterpret_cast<uint4*>(rows) + r * chunks;
 #pragma unroll
             for (int i = 0; i < kSpreadChunks; ++i) {
                 const int c = part * kSpreadUnit + 32 * i + lane;
-                if (c < chunks) dst[c] = v[i];
+                if (c < chunks) rows[r * chunks + c] = v[i];
             }
         }
     }
-    zero_pad_rows(b.off, b.pad, E, chunks, bound, reinterpret_cast<uint4*>(rows), Q8 ? nullptr : prob_row);
+    zero_pad_rows(b, E, chunks, bound, rows, prob_row);
+}
+
+// The last step by token (launch_finish_rows), one pass over its rows: they are
+// read as dx, summed (j ascending, fp32), and written as x. A warp owns a unit of
+// one token's row, so no other thread reads or writes what it does; the k loads
+// of a column chunk are issued together. The unit of a token's first columns also
+// sums its routing weights' gradients: the 32 / KB lanes of an assignment take
+// every so many-th partial, a butterfly adds theirs, a fixed order.
+// In one launch for k = 8 (4096 x 2048) 54 us, for k = 1 (8192 x 5120) 51; as three (the
+// token sum, the weights' sums, x by row) 27 + 4 + 26 and 30 + 5 + 27.
+template <int KB, int CH>
+__global__ void __launch_bounds__(kThreads, KB > 8 ? 2 : 4)
+    finish_rows_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
+                       const int32_t* __restrict__ offsets, int64_t T, int k, int E, int H, uint4* rows,
+                       const int32_t* __restrict__ pad_row, const float* __restrict__ row_dot, int nq,
+                       uint4* __restrict__ dx, float* __restrict__ dprob) {
+    constexpr unsigned kFull = 0xFFFFFFFFu;
+    __shared__ PadBlocks b;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int chunks = H / 8, S = rows8_blocks(H);
+    const int per_row = (chunks + (32 * CH) - 1) / (32 * CH);
+    const int64_t A = T * k, bound = pad16_rows(A, E);
+    const int64_t units = T * per_row, nwarps = ((int64_t)gridDim.x * kThreads) >> 5;
+    pad_blocks(b, offsets, E, A);
+    for (int64_t u = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; u < units; u += nwarps) {
+        int64_t t;
+        int part;
+        split_unit(u, per_row, t, part);
+        const int32_t mine = lane < k ? __ldg(pad_row + t * k + lane) : -1;   // -1: recorded by spread_rows_kernel
+        int32_t r[KB];
+#pragma unroll
+        for (int j = 0; j < KB; ++j) r[j] = __shfl_sync(kFull, mine, j);   // -1 from k on
+        // all loads of the unit before the first store: the rows are read and written
+        uint4 v[CH][KB];
+        uint2 xq[CH];
+        uint32_t xb[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = part * (32 * CH) + 32 * i + lane;
+            if (c >= chunks) continue;
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+                if (r[j] >= 0) v[i][j] = rows[(int64_t)r[j] * chunks + c];
+            xq[i] = __ldg(reinterpret_cast<const uint2*>(q + t * H) + c);
+            xb[i] = __ldg(scale + t * S + (c >> 2));
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int c = part * (32 * CH) + 32 * i + lane;
+            if (c >= chunks) continue;
+            float acc[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) acc[n] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                if (r[j] < 0) continue;
+                const uint32_t w[4] = {v[i][j].x, v[i][j].y, v[i][j].z, v[i][j].w};
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float2 f = unpack_bf16x2(w[n]);
+                    acc[2 * n] += f.x;
+                    acc[2 * n + 1] += f.y;
+                }
+            }
+            dx[t * chunks + c] = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
+                                            pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
+            const uint4 xv = rows8_dequantize8(xq[i], xb[i]);
+#pragma unroll
+            for (int j = 0; j < KB; ++j)
+                if (r[j] >= 0) rows[(int64_t)r[j] * chunks + c] = xv;
+        }
+        if (part == 0) {
+            constexpr int G = 32 / KB;   // lanes of an assignment
+            const int j = lane / G;
+            const int64_t row = __shfl_sync(kFull, mine, j);
+            float sum = 0.0f;
+            if (row >= 0) {
+#pragma unroll 4
+                for (int p = lane % G; p < nq; p += G) sum += __ldg(row_dot + row * nq + p);
+            }
+#pragma unroll
+            for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+            if (lane % G == 0 && j < k) dprob[t * k + j] = sum;
+        }
+    }
+    zero_pad_rows(b, E, chunks, bound, rows, nullptr);
 }
 
 // Blocks for a warp-per-unit kernel: enough warps for every unit, at most `cap`
@@ -277,21 +352,22 @@ cudaError_t launch_spread_rows(const bf16* src, const int32_t* row_of, const int
                                int32_t* pad_row, cudaStream_t st, unsigned* err) {
     if (T == 0) return cudaSuccess;
     const int64_t units = T * ((H / 8 + kSpreadUnit - 1) / kSpreadUnit);
-    return launch_chained(spread_rows_kernel<false>, dim3(unit_blocks(units, resident_blocks())), dim3(kThreads), 0, st,
-                          static_cast<const void*>(src), static_cast<const uint8_t*>(nullptr), row_of, offsets, prob,
-                          T, k, E, H, rows, prob_row, pad_offsets, pad_row, err);
+    return launch_chained(spread_rows_kernel, dim3(unit_blocks(units, resident_blocks())), dim3(kThreads), 0, st,
+                          reinterpret_cast<const uint4*>(src), row_of, offsets, prob, T, k, E, H,
+                          reinterpret_cast<uint4*>(rows), prob_row, pad_offsets, pad_row, err);
 }
 
-cudaError_t launch_spread_rows8(const uint8_t* q, const uint8_t* scale, const int32_t* offsets, int64_t T, int k,
-                                int E, int H, bf16* rows, const int32_t* pad_offsets, const int32_t* pad_row,
-                                cudaStream_t st) {
+cudaError_t launch_finish_rows(const Rows8& x8, const int32_t* offsets, int64_t T, int k, int E, int H, bf16* rows,
+                               const int32_t* pad_row, const float* row_dot, int nq, bf16* dx, float* dprob,
+                               cudaStream_t st) {
     if (T == 0) return cudaSuccess;
-    const int64_t units = T * ((H / 8 + kSpreadUnit - 1) / kSpreadUnit);
-    return launch_chained(spread_rows_kernel<true>, dim3(unit_blocks(units, resident_blocks())), dim3(kThreads), 0, st,
-                          static_cast<const void*>(q), scale, static_cast<const int32_t*>(nullptr), offsets,
-                          static_cast<const float*>(nullptr), T, k, E, H, rows, static_cast<float*>(nullptr),
-                          const_cast<int32_t*>(pad_offsets), const_cast<int32_t*>(pad_row),
-                          static_cast<unsigned*>(nullptr));
+    const int unit = k <= 2 ? 64 : 32;   // chunks of a warp's unit
+    const int64_t units = T * ((H / 8 + unit - 1) / unit);
+    auto kern = k <= 2 ? finish_rows_kernel<2, 2>
+              : k <= 4 ? finish_rows_kernel<4, 1> : k <= 8 ? finish_rows_kernel<8, 1> : finish_rows_kernel<16, 1>;
+    return launch_chained(kern, dim3(unit_blocks(units, resident_blocks() / 2)), dim3(kThreads), 0, st,
+                          static_cast<const uint8_t*>(x8.q), static_cast<const uint8_t*>(x8.scale), offsets, T, k, E,
+                          H, reinterpret_cast<uint4*>(rows), pad_row, row_dot, nq, reinterpret_cast<uint4*>(dx), dprob);
 }
 
 }  // namespace moe
