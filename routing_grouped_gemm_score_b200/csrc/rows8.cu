@@ -154,19 +154,19 @@ __device__ __forceinline__ void zero_pad_rows(const PadBlocks& b, int E, int chu
     for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; i < 16 * (int64_t)E; i += nwarps) {
         const int e = (int)(i >> 4);
         const int64_t r = (int64_t)b.pad[e] + max(b.off[e + 1] - b.off[e], 0) + (i & 15);
-        if (r >= b.pad[e + 1] || r >= bound) continue;
+        if (r < 0 || r >= b.pad[e + 1] || r >= bound) continue;   // < 0: offsets whose sum passed 2^31
         for (int c = lane; c < chunks; c += 32) rows[r * chunks + c] = make_uint4(0, 0, 0, 0);
         if (prob_row != nullptr && lane == 0) prob_row[r] = 0.0f;
     }
 }
 
 // One token's row to the k padded rows of its assignments. Each token's row is
-// read once. A warp owns a unit of one token's row (512 columns: with 1024, 8192
-// rows of 5120 from 8 bits took 34 us against 27); lane j finds the row of
-// assignment j: the expert of row_of[t, j] by bisection of the blocks' offsets,
+// read once. A warp owns a unit of one token's row (512 columns); lane j finds the
+// row of assignment j: the expert of row_of[t, j] by bisection of the blocks' offsets,
 // then its place in the padded block. The unit of a token's first columns writes
 // pad_row and prob_row, and the first block pad_offsets. A row outside its range
-// is recorded and skipped (pad_row -1).
+// is recorded and skipped (pad_row -1). 4096 tokens of 2048 columns, k = 8: 25-29 us
+// (134 MB written), 8192 of 5120, k = 1: 31 us (84 MB read, 84 written).
 __global__ void __launch_bounds__(kThreads)
     spread_rows_kernel(const uint4* __restrict__ src, const int32_t* __restrict__ row_of,
                        const int32_t* __restrict__ offsets, const float* __restrict__ prob, int64_t T, int k, int E,

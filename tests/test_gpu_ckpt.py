@@ -107,6 +107,17 @@ def test_forward_and_backward(T, H, I, E, k, tiles):
     check_backward(d, st, g)
 
 
+@pytest.mark.parametrize("T,H,E,k", [(5000, 1032, 3, 2), (2400, 2056, 8, 7), (1400, 1032, 16, 16)])
+def test_more_units_than_warps(T, H, E, k):
+    """Rows of several units each, more of them than the steps by token have warps."""
+    require_gpu()
+    d = case(T, H, 8, E, k)
+    _, st = forward(d)
+    g = backward(d, st)
+    status_ok()
+    check_backward(d, st, g)
+
+
 @pytest.mark.parametrize("T,H,k", [(9, 40, 2), (300, 264, 3), (70, 4096, 4), (33, 4104, 2), (5, 8192, 1), (400, 5120, 16)])
 @pytest.mark.parametrize("permute", ["auto", "warp"])
 def test_x8_from_every_permute(T, H, k, permute):
