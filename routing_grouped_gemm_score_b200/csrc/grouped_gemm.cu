@@ -83,7 +83,19 @@ constexpr int kStageHalfP = 64 * BK * 2 + kStageBP;
 // expert's down GEMM, whose output rows are the tokens in order).
 // kEpiSwigluBwd8: the SwiGLU backward from g and u saved in 8 bits, which also
 // recomputes h for the weight gradient of the down GEMM.
-enum Epi { kEpiStore = 0, kEpiSwiglu = 1, kEpiSwigluBwd = 2, kEpiStoreAdd = 3, kEpiSwigluBwd8 = 4 };
+// kEpiSwiglu8: the SwiGLU forward that saves g and u in 8 bits. A kernel of its own,
+// not a branch of kEpiSwiglu: that branch, not taken, made the swap-AB forward of 64
+// rows a tile 15.8 us instead of 8.9 (T = 64, H = 128) and the one-launch MLP 46 instead
+// of 41 (T = 64, skewed, H = 2048, I = 768, 128 experts).
+enum Epi {
+    kEpiStore = 0,
+    kEpiSwiglu = 1,
+    kEpiSwigluBwd = 2,
+    kEpiStoreAdd = 3,
+    kEpiSwigluBwd8 = 4,
+    kEpiSwiglu8 = 5
+};
+constexpr bool swiglu_forward(int epi) { return epi == kEpiSwiglu || epi == kEpiSwiglu8; }
 
 struct Params {
     int groups;           // number of experts
@@ -101,8 +113,8 @@ struct Params {
     int64_t ldo2;
     const bf16* aux;           // SwiGLU backward: the saved [g | u]
     int64_t ld_aux;
-    // [g | u] in 8 bits (rows8.cuh), written by the SwiGLU forward (NULL: skip)
-    // and read by kEpiSwigluBwd8: values [rows][2I], scale bytes [2 S][rows],
+    // [g | u] in 8 bits (rows8.cuh), written by kEpiSwiglu8 and read by
+    // kEpiSwigluBwd8: values [rows][2I], scale bytes [2 S][rows],
     // S = ceil(I / 32), the blocks of g first. Block-major scales, because a
     // lane holds a row: a warp's 32 bytes of one block are one sector.
     uint8_t* gu8;
@@ -295,7 +307,7 @@ __device__ __forceinline__ Tile decode_tile(const S& s, const Params& p, int id,
 // for 256-row and 128-row tiles alike.
 template <int EPI>
 __device__ __forceinline__ int b_col_1cta(const Tile& t, const Params& p, int c) {
-    if (EPI == kEpiSwiglu) {
+    if (swiglu_forward(EPI)) {
         const int n0 = t.n_blk * (BN / 2);
         return (c < 2) ? n0 + 64 * c : p.I + n0 + 64 * (c - 2);
     }
@@ -304,7 +316,7 @@ __device__ __forceinline__ int b_col_1cta(const Tile& t, const Params& p, int c)
 
 template <int EPI>
 __device__ __forceinline__ int b_col_pair(const Tile& t, const Params& p, uint32_t rank, int c) {
-    if (EPI == kEpiSwiglu) return (c == 0 ? 0 : p.I) + t.n_blk * (BN / 2) + 64 * (int)rank;
+    if (swiglu_forward(EPI)) return (c == 0 ? 0 : p.I) + t.n_blk * (BN / 2) + 64 * (int)rank;
     return t.n_blk * BN + (int)rank * 128 + 64 * c;
 }
 
@@ -613,7 +625,7 @@ struct EpiMap {
 // forward: gate in columns [0, 128), up in [128, 256).
 template <int EPI>
 __device__ __forceinline__ EpiMap full_map(int warp_r0, int col_half) {
-    if (EPI == kEpiSwiglu) return EpiMap{warp_r0, 64 * col_half, 2, 64 * col_half, BN / 2};
+    if (swiglu_forward(EPI)) return EpiMap{warp_r0, 64 * col_half, 2, 64 * col_half, BN / 2};
     return EpiMap{warp_r0, 128 * col_half, 4, 128 * col_half, 0};
 }
 
@@ -622,7 +634,7 @@ __device__ __forceinline__ EpiMap full_map(int warp_r0, int col_half) {
 // the same for the next 64 (CTA 1's).
 template <int EPI>
 __device__ __forceinline__ EpiMap pair_full_map(int warp_r0, int col_half) {
-    if (EPI == kEpiSwiglu) return EpiMap{warp_r0, 64 * col_half, 2, 128 * col_half, 64};
+    if (swiglu_forward(EPI)) return EpiMap{warp_r0, 64 * col_half, 2, 128 * col_half, 64};
     return full_map<EPI>(warp_r0, col_half);
 }
 
@@ -635,7 +647,7 @@ __device__ __forceinline__ EpiMap pair_full_map(int warp_r0, int col_half) {
 template <int EPI>
 __device__ __forceinline__ EpiMap half_map(uint32_t rank, int quarter, int col_half) {
     const int r0 = 64 * (int)rank + 32 * (quarter & 1);
-    if (EPI == kEpiSwiglu) return EpiMap{r0, 64 * (quarter >> 1) + 32 * col_half, 1, 32 * col_half, 64};
+    if (swiglu_forward(EPI)) return EpiMap{r0, 64 * (quarter >> 1) + 32 * col_half, 1, 32 * col_half, 64};
     return EpiMap{r0, 128 * (quarter >> 1) + 64 * col_half, 2, 64 * col_half, 0};
 }
 
@@ -651,7 +663,7 @@ __device__ __forceinline__ void epilogue_tile(const Params& p, const Tile& t, ui
                                               const CUtensorMap* tmC2, typename EpiAux<EPI>::type* pre) {
     const int warp_r0 = em.r0;
     const int r = warp_r0 + lane;
-    if (EPI == kEpiSwiglu) {
+    if (swiglu_forward(EPI)) {
         const int n0 = t.n_blk * (n_tile / 2);
         const int nvalid = min(max(t.rows - warp_r0, 0), 32);
         const int64_t row0 = (int64_t)t.row0 + warp_r0;
@@ -667,13 +679,7 @@ __device__ __forceinline__ void epilogue_tile(const Params& p, const Tile& t, ui
             // columns of the chunk inside the output (a multiple of 8): a partial chunk takes
             // masked row stores, since a TMA store of the g part would spill into the u columns
             const int ncols = min(32, p.N - (n0 + c0));
-            if (p.out2) {
-                put_block32(buf, p.out2 + row0 * p.ldo2 + n0 + c0, p.ldo2, nvalid, ncols, g, lane, tmC2, n0 + c0,
-                            (int)row0);
-                put_block32(buf, p.out2 + row0 * p.ldo2 + p.I + n0 + c0, p.ldo2, nvalid, ncols, u, lane, tmC2,
-                            p.I + n0 + c0, (int)row0);
-            }
-            if (p.gu8) {
+            if constexpr (EPI == kEpiSwiglu8) {
                 // one rounding, from the fp32 accumulator
                 uint32_t g8[8], u8[8];
                 const uint32_t g_byte = quantize_block32(g, ncols, g8), u_byte = quantize_block32(u, ncols, u8);
@@ -687,6 +693,11 @@ __device__ __forceinline__ void epilogue_tile(const Params& p, const Tile& t, ui
                 uint8_t* q = p.gu8 + row0 * 2 * p.I + n0 + c0;
                 store_rows8_32(buf, q, 2 * (int64_t)p.I, nvalid, ncols, true, g8, lane);
                 store_rows8_32(buf + 1024, q + p.I, 2 * (int64_t)p.I, nvalid, ncols, (p.I & 15) == 0, u8, lane);
+            } else if (p.out2) {
+                put_block32(buf, p.out2 + row0 * p.ldo2 + n0 + c0, p.ldo2, nvalid, ncols, g, lane, tmC2, n0 + c0,
+                            (int)row0);
+                put_block32(buf, p.out2 + row0 * p.ldo2 + p.I + n0 + c0, p.ldo2, nvalid, ncols, u, lane, tmC2,
+                            p.I + n0 + c0, (int)row0);
             }
 #pragma unroll
             for (int i = 0; i < 32; ++i) g[i] = silu_f(g[i]) * u[i] * rs;     // h, in place
@@ -868,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA64,
                      const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmC,
                      const __grid_constant__ CUtensorMap tmC2, const Params p) {
-    static_assert(EPI != kEpiSwiglu || B_MN, "the SwiGLU forward reads its weight N-major");
+    static_assert(!swiglu_forward(EPI) || B_MN, "the SwiGLU forward reads its weight N-major");
     extern __shared__ uint8_t smem_raw[];
     SmemP& s = *reinterpret_cast<SmemP*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                          ~uintptr_t(1023));
@@ -1661,16 +1672,16 @@ static_assert(sizeof(SmemS<16>) + 1024 <= 227 * 1024 && sizeof(SmemS<64>) + 1024
 // First weight column of chunk c (0, 1) of the tile's 128 columns.
 template <int EPI>
 __device__ __forceinline__ int w_col_swap(const Tile& t, const Params& p, int c) {
-    if (EPI == kEpiSwiglu) return (c == 0 ? 0 : p.I) + t.n_blk * 64;
+    if (swiglu_forward(EPI)) return (c == 0 ? 0 : p.I) + t.n_blk * 64;
     return t.n_blk * 128 + 64 * c;
 }
 
 // Epilogue of a swap-AB SwiGLU tile for one warp: v holds the warp's kWC token
 // columns (j0 ..) of its lane's weight column. The warps of the upper lane
 // quarters (u) hand their values to those of the lower quarters (g) through
-// ubuf, which store h = silu(g) u (times the row scale) and [g | u]. Returns
-// false if the hand-over wait gave up.
-template <int NR>
+// ubuf, which store h = silu(g) u (times the row scale) and [g | u] (in 8 bits with
+// SAVE8, else in bf16 if asked for). Returns false if the hand-over wait gave up.
+template <int NR, bool SAVE8>
 __device__ __forceinline__ bool swap_epi_swiglu(SmemS<NR>& s, const Params& p, const Tile& t, int buf,
                                                 uint32_t use, int quarter, int j0, int lane,
                                                 const float (&v)[SwapCfg<NR>::kWarpCols], volatile int* abort_flag) {
@@ -1689,7 +1700,7 @@ __device__ __forceinline__ bool swap_epi_swiglu(SmemS<NR>& s, const Params& p, c
     const int hc = t.n_blk * 64 + 32 * quarter + lane;   // column of h
     const float* urow = s.ubuf[buf][32 * quarter + lane] + j0;
     const int64_t r0 = (int64_t)t.row0 + j0;
-    if (p.gu8) {
+    if constexpr (SAVE8) {
         // The warp's 32 lanes hold one block of 32 columns of every row. Its
         // largest finite magnitude: bit patterns of non-negative floats order as
         // the floats do, so an integer maximum over the warp finds it.
@@ -1714,7 +1725,7 @@ __device__ __forceinline__ bool swap_epi_swiglu(SmemS<NR>& s, const Params& p, c
         if (i >= nvalid || hc >= p.N) break;
         const float g = v[i], u = urow[i];
         const float rs = p.row_scale ? __ldg(p.row_scale + r0 + i) : 1.0f;
-        if (p.out2) {
+        if (!SAVE8 && p.out2) {
             p.out2[(r0 + i) * p.ldo2 + hc] = __float2bfloat16_rn(g);
             p.out2[(r0 + i) * p.ldo2 + p.I + hc] = __float2bfloat16_rn(u);
         }
@@ -1745,7 +1756,7 @@ template <int EPI, int NR>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_swap_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                      const Params p) {
-    static_assert(EPI == kEpiSwiglu || EPI == kEpiStore, "forward GEMMs only");
+    static_assert(swiglu_forward(EPI) || EPI == kEpiStore, "forward GEMMs only");
     extern __shared__ uint8_t smem_raw[];
     using Cfg = SwapCfg<NR>;
     SmemS<NR>& s = *reinterpret_cast<SmemS<NR>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -1881,7 +1892,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             else tmem_load_8(taddr, v);
             const int j0 = kWC * half;                       // first token column of this warp
             bool ok = true;
-            if (EPI == kEpiSwiglu) ok = swap_epi_swiglu<NR>(s, p, t, buf, use, quarter, j0, lane, v, abort_flag);
+            if constexpr (swiglu_forward(EPI))
+                ok = swap_epi_swiglu<NR, EPI == kEpiSwiglu8>(s, p, t, buf, use, quarter, j0, lane, v, abort_flag);
             else swap_epi_store<NR>(p.out, p.ldo, p.N, t, quarter, j0, lane, v);
             tc_fence_before();
             __syncwarp();
@@ -1913,7 +1925,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the epilogue warps of all gate_up tiles of its expert have stored their
 // part of h and counted themselves in sched[1 + g], and then issues the loads
 // of h. Each expert must hold at most NR rows (one row block); otherwise the
-// launch records a device-check error and computes nothing.
+// launch records a device-check error and computes nothing. SAVE8: [g | u] is saved
+// in 8 bits (see kEpiSwiglu8).
 template <int NR>
 __device__ __forceinline__ Tile decode_mlp_tile(const SmemS<NR>& s, const Params& p, int id, int total1,
                                                 bool& down) {
@@ -1927,7 +1940,7 @@ __device__ __forceinline__ Tile decode_mlp_tile(const SmemS<NR>& s, const Params
     return t;
 }
 
-template <int NR>
+template <int NR, bool SAVE8>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_swap_mlp_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmWgu,
                          const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmWd,
@@ -2129,7 +2142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int j0 = kWC * half;
             bool ok = true;
             if (!down) {
-                ok = swap_epi_swiglu<NR>(s, p, t, buf, use, quarter, j0, lane, v, abort_flag);
+                ok = swap_epi_swiglu<NR, SAVE8>(s, p, t, buf, use, quarter, j0, lane, v, abort_flag);
                 if (ok && quarter < 2) {
                     // this warp's part of expert g's h is stored: make it visible to
                     // other CTAs' TMA loads, then count it
@@ -2328,10 +2341,10 @@ cudaError_t launch_wgrad_pair(const CUtensorMap& a, const CUtensorMap& b, const 
     return launch_clusters(gemm_wgrad_pair_kernel, max_tiles, kThreads, kSmemWBytes, st, a, b, c, p);
 }
 
-template <int NR>
+template <int NR, bool SAVE8>
 cudaError_t launch_mlp(const CUtensorMap& x_rows, const CUtensorMap& w_gate_up, const CUtensorMap& h_rows,
                        const CUtensorMap& w_down, const Params& p, int64_t grid, cudaStream_t st) {
-    auto kern = gemm_swap_mlp_kernel<NR>;
+    auto kern = gemm_swap_mlp_kernel<NR, SAVE8>;
     static PerDeviceFlag configured;
     if (const cudaError_t e = allow_smem(kern, swap_smem_bytes<NR>(), configured); e != cudaSuccess) return e;
     return launch_chained(kern, dim3((unsigned)grid), dim3(kThreads), swap_smem_bytes<NR>(), st, x_rows, w_gate_up,
@@ -2416,11 +2429,13 @@ cudaError_t gemm_gate_up_swiglu(const bf16* x, int64_t rows, const int32_t* offs
     p.row_scale = row_scale;
     if (use_swap_tiles(rows, groups)) {
         p.n_blocks = (I + 63) / 64;   // 64 gate and the matching 64 up columns per tile
-        return launch_swap_rows<kEpiSwiglu>(x, rows, H, max_group_rows, tb, p, st);
+        return gu8.q ? launch_swap_rows<kEpiSwiglu8>(x, rows, H, max_group_rows, tb, p, st)
+                     : launch_swap_rows<kEpiSwiglu>(x, rows, H, max_group_rows, tb, p, st);
     }
     CUtensorMap tc, tc2;
     if (!make_out_map(&tc, h, rows, I)) return cudaErrorInvalidValue;
     if (gu_save && !make_out_map(&tc2, gu_save, rows, 2 * (uint64_t)I)) return cudaErrorInvalidValue;
+    if (gu8.q) return launch_group_m<kEpiSwiglu8, true>(ta, ta64, tb, tb, p, st, &tc);
     return launch_group_m<kEpiSwiglu, true>(ta, ta64, tb, tb, p, st, &tc, gu_save ? &tc2 : nullptr);
 }
 
@@ -2454,8 +2469,9 @@ cudaError_t gemm_gate_up_swiglu_gather(const bf16* x, int64_t T, const int32_t* 
     CUtensorMap tc, tc2;
     if (!make_out_map(&tc, h, rows, I)) return cudaErrorInvalidValue;
     if (gu_save && !make_out_map(&tc2, gu_save, rows, 2 * (uint64_t)I)) return cudaErrorInvalidValue;
-    return launch_1cta<kEpiSwiglu, false, true, false>(ta, tb, p, single_tile_bound(rows, E, p.n_blocks), st, &tc,
-                                                       gu_save ? &tc2 : nullptr);
+    const int64_t tiles = single_tile_bound(rows, E, p.n_blocks);
+    if (gu8.q) return launch_1cta<kEpiSwiglu8, false, true, false>(ta, tb, p, tiles, st, &tc);
+    return launch_1cta<kEpiSwiglu, false, true, false>(ta, tb, p, tiles, st, &tc, gu_save ? &tc2 : nullptr);
 }
 
 bool use_fused_mlp(int64_t rows, int groups, int64_t max_group_rows, int I) {
@@ -2506,7 +2522,9 @@ cudaError_t gemm_expert_mlp_fused(const bf16* x, int64_t rows, const int32_t* of
     const int64_t experts = rows < E ? rows : E;
     int64_t grid = experts * (p.n_blocks + p.n_blocks2);
     if (grid > sm_count()) grid = sm_count();
-    return nr == 16 ? launch_mlp<16>(tx, twgu, th, twd, p, grid, st) : launch_mlp<64>(tx, twgu, th, twd, p, grid, st);
+    const auto launch = gu8.q ? (nr == 16 ? launch_mlp<16, true> : launch_mlp<64, true>)
+                              : (nr == 16 ? launch_mlp<16, false> : launch_mlp<64, false>);
+    return launch(tx, twgu, th, twd, p, grid, st);
 }
 
 bool grouped_gemm_single_tiles(int64_t rows, int groups) {

@@ -197,8 +197,8 @@ cudaError_t launch_rmsnorm_backward(const bf16* dy, const bf16* s, const bf16* w
 // Grouped GEMMs on tcgen05. Each returns cudaErrorInvalidValue if a tensor
 // map cannot be encoded (bad alignment or extent).
 // gate_up + SwiGLU: h[r] = silu(x[r] Wg[e]) * (x[r] Wu[e]); optionally gu[r] = [g | u]
-// in bf16 (gu_save) and, from the fp32 accumulators, in 8 bits (gu8: two parts of I
-// columns, block-major scales).
+// in bf16 (gu_save) or, from the fp32 accumulators, in 8 bits (gu8: two parts of I
+// columns, block-major scales; gu_save is then not written).
 // offsets NULL: one group of `rows` rows using the weights of group 0.
 // max_group_rows: an upper bound on the rows of any group (0: rows), which
 // lets small batches take narrower swap-AB tiles (a layer call passes T: a
