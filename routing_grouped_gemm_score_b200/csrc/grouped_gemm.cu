@@ -2299,16 +2299,18 @@ int64_t single_tile_bound(int64_t rows, int groups, int n_blocks) {
 // 1326 us), and slower at 256 (Qwen3-30B-A3B shape: 321 against 286 us).
 // moe_testing_set_kernels can force either kind (the tests run both kernels
 // on the same shapes).
-// The gate_up dgrad, a plain store of a long reduction, gains from pair tiles
-// earlier (kPairRowsDgrad): 220 against 224 us at 256 rows per expert (Qwen3-30B-
-// A3B; the whole backward 907 against 915), 1152 against 1157 at 512 (Llama-4; 4037
-// against 4096). Below 128 rows a block is one half-filled pair tile on two SMs.
-constexpr int64_t kPairRows = 1024, kPairRowsDgrad = 192;
-bool use_pair_tiles(int64_t rows, int groups, int64_t rows_per_group = kPairRows) {
+// The gate_up dgrad goes by the same number. Between 192 and 768 rows per expert pair
+// tiles have no rule that holds there, pair against single: Qwen3-30B-A3B widths 181
+// against 202 us (192 rows, even routing) but 316 against 277 (320) and 3 to 5 % slower
+// throughout with uneven routing; Llama-4 589 against 640 (192) but 835 against 769
+// (256); Mixtral 732 against 835 (384) but 925 against 849 (512); 8 experts of 1024 x
+// 512, 512 rows: 31.7 against 23.6.
+constexpr int64_t kPairRows = 1024;
+bool use_pair_tiles(int64_t rows, int groups) {
     const int forced = kernel_override().gemm_tiles;
     if (forced == MOE_TESTING_GEMM_PAIR) return true;
     if (forced != MOE_TESTING_AUTO) return false;
-    return groups == 1 || rows >= (int64_t)groups * rows_per_group;
+    return groups == 1 || rows >= (int64_t)groups * kPairRows;
 }
 
 // The forward GEMMs take swap-AB tiles (weights as the 128-row operand, 64
@@ -2385,9 +2387,8 @@ cudaError_t launch_swap_rows(const bf16* x, int64_t rows, int K, int64_t max_gro
 template <int EPI, bool B_MN>
 cudaError_t launch_group_m(const CUtensorMap& ta, const CUtensorMap& ta64, const CUtensorMap& tb_pair,
                            const CUtensorMap& tb_single, const Params& p, cudaStream_t st,
-                           const CUtensorMap* out_map, const CUtensorMap* out2_map = nullptr,
-                           int64_t pair_rows = kPairRows) {
-    if (use_pair_tiles(p.rows, p.groups, pair_rows))
+                           const CUtensorMap* out_map, const CUtensorMap* out2_map = nullptr) {
+    if (use_pair_tiles(p.rows, p.groups))
         return launch_pair<EPI, B_MN>(ta, ta64, tb_pair, p, pair_tile_bound(p.rows, p.groups, p.n_blocks), st,
                                       out_map, out2_map);
     return launch_1cta<EPI, false, B_MN, false>(ta, tb_single, p,
@@ -2669,7 +2670,7 @@ cudaError_t gemm_gate_up_dgrad(const bf16* dgu, int64_t rows, const int32_t* off
     p.ldo = H;
     CUtensorMap tc;
     if (!make_out_map(&tc, dx_perm, rows, H)) return cudaErrorInvalidValue;
-    return launch_group_m<kEpiStore, false>(ta, ta64, tb, tb1, p, st, &tc, nullptr, kPairRowsDgrad);
+    return launch_group_m<kEpiStore, false>(ta, ta64, tb, tb1, p, st, &tc);
 }
 
 cudaError_t gemm_wgrad(const bf16* X, const bf16* D, int64_t rows, const int32_t* offsets, int E,

@@ -36,3 +36,26 @@ def test_the_plain_forward_has_kernels_of_its_own(T, H, I, E, k):
     gemms = [n for n in plain if "gemm" in n]
     assert len(gemms) in (1, 2)   # one launch for the MLP, or gate_up and down
     assert len([n for n in gemms if n in ckpt]) == len(gemms) - 1   # the down GEMM alone is the same
+
+
+# rows an expert: the gate_up dgrad takes CTA pairs where the other group-M products do,
+# in every backward (from 1024 rows an expert on)
+@pytest.mark.parametrize("T,E,k,pairs", [(512, 4, 2, 0), (1024, 4, 2, 0), (1500, 2, 2, 2)])
+def test_tiles_of_the_dgrads(T, E, k, pairs):
+    require_gpu()
+    import routing_grouped_gemm_score_b200 as m
+    H, I = 128, 64
+    d = case(T, H, I, E, k)
+    c = d["cuda"]
+    w = (c["w_gate_up"], c["w_down"])
+    _, st = m.moe_layer_forward(c["logits"], c["x"], *w, k, opts(d), save_for_backward=True)
+    p = m.moe_permute(c["x"], st["topk_idx"], st["offsets"])
+    scale = torch.empty(T * k, device="cuda")
+    scale[p["row_of"].reshape(-1).long()] = st["topk_prob"].reshape(-1)
+    h = m.moe_grouped_mlp_scaled(p["x_perm"], st["offsets"], *w, scale, save=True)
+    _, st8 = forward(d)
+    for call in (lambda: m.moe_grouped_mlp_backward(c["dout"], st, *w),
+                 lambda: m.moe_grouped_mlp_scaled_backward(c["dout"], p["row_of"], p["sorted_token"], scale,
+                                                           st["offsets"], p["x_perm"], h["gu"], h["h"], *w),
+                 lambda: backward(d, st8)):
+        assert sum("gemm_pair_kernel" in n for n in launched(call)) == pairs
