@@ -147,7 +147,8 @@ moe_status moe_dequantize_rows(const uint8_t* q, const uint8_t* scale, int64_t r
  *  eps       >= 0; with eps = 0 a row of zeros gives NaN, as the formula does
  *  sum       out bf16 [T, H], s (NULL: not stored; needs a residual). May be x
  *            or residual itself
- *  y         out bf16 [T, H] (NULL: not stored). May be x itself
+ *  y         out bf16 [T, H] (NULL: not stored). May be x itself, if sum is not;
+ *            sum and y must not overlap (MOE_ERR_INVALID_ARG)
  *  y_q       out uint8 [T, H], y_scale out uint8 [T, ceil(H / 32)] (both NULL: not
  *            stored; one of y and y_q is needed)
  *  rstd      out fp32 [T] (NULL: not stored)

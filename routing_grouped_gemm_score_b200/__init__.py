@@ -700,9 +700,10 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Opt
     bf16; x itself without a residual), rstd (fp32 [T]) and, with quantize, y_q and
     y_scale, y in the 8-bit format (the x8 of moe_layer_forward_ckpt). sum and
     rstd are what moe_rmsnorm_backward needs. `out`: preallocated tensors by those
-    names ("sum" may be x or residual itself, for an update in place); what it does
-    not hold is allocated, except that an entry that is None is not computed (sum,
-    rstd, or y next to the 8-bit output)."""
+    names ("sum" may be x or residual itself, for an update in place, and "y" may be x
+    if "sum" is not; without a residual nothing then holds the sum, which is None);
+    what it does not hold is allocated, except that an entry that is None is not
+    computed (sum, rstd, or y next to the 8-bit output)."""
     _need(x, torch.bfloat16, "x")
     if x.dim() != 2:
         raise ValueError(f"x must have two dimensions, got {tuple(x.shape)}")
@@ -730,6 +731,8 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Opt
         s = x   # without a residual nothing is stored
         if residual is not None:
             s = r["sum"] if "sum" in r else torch.empty_like(x)
+        elif y is not None and T > 0 and y.data_ptr() == x.data_ptr():
+            s = None
         q = scale = None
         if quantize:
             q = r["y_q"] if "y_q" in r else torch.empty_like(x, dtype=torch.uint8)

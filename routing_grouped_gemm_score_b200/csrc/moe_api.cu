@@ -942,6 +942,8 @@ moe_status moe_rmsnorm(const moe_bf16* x, const moe_bf16* residual, const moe_bf
     const void* all[] = {x, residual, weight, sum, y, y_q, y_scale, rstd};
     for (const void* p : all)
         if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
+    const uintptr_t s0 = reinterpret_cast<uintptr_t>(sum), y0 = reinterpret_cast<uintptr_t>(y);
+    if (sum && y && (s0 < y0 ? y0 - s0 : s0 - y0) < (size_t)T * (size_t)H * sizeof(bf16)) return MOE_ERR_INVALID_ARG;
     auto B = [](const moe_bf16* p) { return reinterpret_cast<const bf16*>(p); };
     return from_cuda(launch_rmsnorm(B(x), B(residual), B(weight), T, H, eps, reinterpret_cast<bf16*>(sum),
                                     reinterpret_cast<bf16*>(y), y_q, y_scale, rstd,
