@@ -138,9 +138,10 @@ moe_status moe_dequantize_rows(const uint8_t* q, const uint8_t* scale, int64_t r
  *   rstd = (sum_i s_i^2 / H + eps)^(-1/2)        y_i = s_i * rstd * weight_i
  * The stored sum is what is normalised, so moe_rmsnorm_backward, which reads it,
  * differentiates exactly this function, and the call gives the bits of a call
- * without residual on that sum. y is stored in bf16 and, rounded once from the
- * same fp32 value, in 8 bits (the format above, one part, scales by row): the
- * x_q and x_scale of moe_layer_forward_ckpt.
+ * without residual on that sum. A row's results have the same bits whatever T is.
+ * y is stored in bf16 and, rounded once from the same fp32 value, in 8 bits (the
+ * format above, one part, scales by row): the x_q and x_scale of
+ * moe_layer_forward_ckpt.
  *  x         in  bf16 [T, H]
  *  residual  in  bf16 [T, H] (NULL: none)
  *  weight    in  bf16 [H]

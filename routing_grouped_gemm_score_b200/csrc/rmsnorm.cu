@@ -51,15 +51,26 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Forward. One row per block, whose threads hold CH 8-column chunks each. The
+// Threads for a row of that many chunks with ch of them each, whole warps.
+__host__ __device__ constexpr int row_sums(int chunks, int ch) { return ((chunks + ch - 1) / ch + 31) / 32 * 32; }
+
+// Forward. One row per block, whose threads hold CH 8-column chunks each. The squares
+// are added in one order for a given H, so that a row's results do not depend on T, by
+// which CH is chosen: the eight of a chunk; W apart, the OC chunks of one of W sums; 32
+// of those by a butterfly; then the warps'. OC and W are the CH and the threads of the
+// kernel for many rows, which adds them in registers; the one for few rows (CH < OC)
+// hands its chunks' sums over in shared memory. (32 chunks by a butterfly each, then
+// these: one order as well, but 127 us instead of 122 for 16384 rows of 5120.) The
 // pointers may alias as documented (sum with x or residual, y with x): a row's
 // elements are read before they are written, by the same thread, so no pointer is
 // marked restrict or read through the non-coherent path.
-template <int CH>
+template <int CH, int OC>
 __global__ void __launch_bounds__(32 * kMaxWarps)
     rmsnorm_kernel(const uint4* x, const uint4* residual, const uint4* weight, int H, float eps, uint4* sum, uint4* y,
                    uint8_t* y_q, uint8_t* y_scale, float* rstd_out) {
+    static_assert(CH <= OC, "the order is the kernel's for many rows, whose threads hold more chunks");
     __shared__ float red[kMaxWarps];
+    __shared__ float chunk_sum[CH < OC ? 32 * kMaxWarps * CH : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int width = (int)blockDim.x, me = (int)threadIdx.x;
     const int64_t t = blockIdx.x;
@@ -89,14 +100,25 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
             if (sum && c < chunks) sum[t * chunks + c] = s;
             unpack8(s, v[i]);
         }
+        float part = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
+        for (int j = 0; j < 8; ++j) part += v[i][j] * v[i][j];
+        if constexpr (CH < OC) chunk_sum[me + i * width] = part;   // absent chunks: 0
+        else ss += part;
+    }
+    int sums = width;   // W
+    if constexpr (CH < OC) {
+        sums = row_sums(chunks, OC);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < OC; ++i)
+            if (me < sums && me + i * sums < chunks) ss += chunk_sum[me + i * sums];
     }
     ss = warp_sum(ss);
     if (lane == 0) red[warp] = ss;
     __syncthreads();
     ss = 0.0f;
-    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) ss += red[i];
+    for (int i = 0; i < (sums >> 5); ++i) ss += red[i];
     const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
     if (rstd_out && me == 0) rstd_out[t] = rstd;
     const int S = rows8_blocks(H);
@@ -308,10 +330,7 @@ __global__ void __launch_bounds__(1024)
 }
 
 // Threads of a block that owns a row with CH chunks a thread.
-int row_threads(int H, int ch) {
-    const int need = (H / 8 + ch - 1) / ch;
-    return (need + 31) / 32 * 32;
-}
+int row_threads(int H, int ch) { return row_sums(H / 8, ch); }
 
 int bwd_chunks(int H) { return H <= 4096 ? 1 : H <= 8192 ? 2 : 4; }
 
@@ -373,11 +392,12 @@ cudaError_t launch_rmsnorm(const bf16* x, const bf16* residual, const bf16* weig
     // 133, 127 and 122 us with 1, 2 and 4 chunks a thread, 4096 rows of 2048 14.3,
     // 13.4 and 13.3. With fewer rows than SMs only the latency of one row counts
     // (2.2, 2.4 and 3.2 us): as many threads as a block may have.
-    const int ch = T < sm_count() ? (chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4)
-                                  : (chunks <= 128 ? 1 : chunks <= 512 ? 2 : 4);
-    if (ch == 1) go(rmsnorm_kernel<1>, rows, row_threads(H, 1));
-    else if (ch == 2) go(rmsnorm_kernel<2>, rows, row_threads(H, 2));
-    else go(rmsnorm_kernel<4>, rows, row_threads(H, 4));
+    const bool few = T < sm_count();
+    if (chunks <= 128) go(rmsnorm_kernel<1, 1>, rows, row_threads(H, 1));
+    else if (chunks <= 512 && few) go(rmsnorm_kernel<1, 2>, rows, row_threads(H, 1));
+    else if (chunks <= 512) go(rmsnorm_kernel<2, 2>, rows, row_threads(H, 2));
+    else if (chunks <= 1024 && few) go(rmsnorm_kernel<2, 4>, rows, row_threads(H, 2));
+    else go(rmsnorm_kernel<4, 4>, rows, row_threads(H, 4));
     return cudaGetLastError();
 }
 
