@@ -154,7 +154,10 @@ moe_status moe_dequantize_rows(const uint8_t* q, const uint8_t* scale, int64_t r
  *            stored; one of y and y_q is needed)
  *  rstd      out fp32 [T] (NULL: not stored)
  * H is a multiple of 8, at most 16384 (MOE_ERR_UNSUPPORTED otherwise); T = 0 is
- * allowed. A row whose sum of squares passes fp32's range gets rstd = 0. */
+ * allowed. A row of any finite size is normalised: where its squares leave fp32's
+ * range, it is scaled by a power of two before they are taken. rstd is fp32: +inf for
+ * a row whose root mean square (with eps) is below 2^-128, of which y is still right
+ * but moe_rmsnorm_backward gives no numbers. */
 moe_status moe_rmsnorm(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* weight, int64_t T,
                        int H, float eps, moe_bf16* sum, moe_bf16* y, uint8_t* y_q, uint8_t* y_scale,
                        float* rstd, void* stream);

@@ -23,6 +23,7 @@ namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kMaxWarps = 16;      // of a block that owns one row
+constexpr float kSmallestMean = 0x1p-100f;   // of squares that are summed without scaling
 constexpr size_t kBwdSmem = 200 * 1024;   // an SM's shared memory for the backward's rings
 // Backward threads an SM: 1024 and 1536 measured alike at 5120 columns (59 us for
 // 8192 rows), and at 2048 (4096 rows) 14.2 + 3.5 against 13.8 + 4.5 us, since more
@@ -54,6 +55,110 @@ __device__ __forceinline__ float warp_sum(float v) {
 // Threads for a row of that many chunks with ch of them each, whole warps.
 __host__ __device__ constexpr int row_sums(int chunks, int ch) { return ((chunks + ch - 1) / ch + 31) / 32 * 32; }
 
+// The rest of the order of a row's sum of squares (rmsnorm_kernel), from each thread's or
+// the chunks' sums; the same in every thread.
+template <int CH, int OC>
+__device__ __forceinline__ float row_sum(float ss, const float* chunk_sum, float* red, int chunks) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = (int)threadIdx.x;
+    const int sums = CH < OC ? row_sums(chunks, OC) : (int)blockDim.x;   // W
+    if constexpr (CH < OC) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < OC; ++i)
+            if (me < sums && me + i * sums < chunks) ss += chunk_sum[me + i * sums];
+    }
+    ss = warp_sum(ss);
+    if (lane == 0) red[warp] = ss;
+    __syncthreads();
+    ss = 0.0f;
+    for (int i = 0; i < (sums >> 5); ++i) ss += red[i];
+    return ss;
+}
+
+// The rest of a row whose squares are past fp32's range, or so small that their roundings
+// count (at a mean of 2^-100 a square is off by 2^-50 of it at most): summed again, scaled
+// by up0 up1, the power of two that takes the larger of the row's magnitude and eps^1/2 to
+// [1, 2). A row with an infinity, or of zeros with eps = 0, stays as it is. The pointers
+// are the row's; its s (or x and residual) is read again, a chunk at a time, and a path of
+// its own keeps the usual one as it is: as a detour before the outputs, from registers,
+// it took 20 more of them, and the norm of 16384 rows of 5120 144 us (124 with the
+// registers capped) instead of 122.
+template <int CH, int OC>
+__device__ __noinline__ void scaled_row(const uint4* s, const uint4* residual, const uint4* weight, int H, float eps,
+                                        uint4* y, uint8_t* y_q, uint8_t* y_scale, float* rstd_out, float* chunk_sum,
+                                        float* red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int width = (int)blockDim.x, me = (int)threadIdx.x, chunks = H / 8;
+    const auto s_chunk = [&](int c, float (&f)[8]) {   // zeros past the row
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        unpack8(c < chunks ? s[c] : none, f);
+        if (residual) {
+            float r[8];
+            unpack8(c < chunks ? residual[c] : none, r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] += r[j];
+            unpack8(pack8(f), f);
+        }
+    };
+    float a = 0.0f, f[8];
+#pragma unroll 1
+    for (int i = 0; i < CH; ++i) {
+        s_chunk(me + i * width, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(f[j]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kFull, a, o));
+    __syncthreads();   // every warp is done with red
+    if (lane == 0) red[warp] = a;
+    __syncthreads();
+    for (int i = 0; i < (width >> 5); ++i) a = fmaxf(a, red[i]);
+    a = fmaxf(a, sqrtf(eps));
+    __syncthreads();
+    float up0 = 1.0f, up1 = 1.0f;
+    if (a > 0.0f && a < INFINITY) {
+        const int k = -ilogbf(a);   // in [-127, 149]: in two factors that fp32 holds
+        up0 = __uint_as_float((uint32_t)(127 + k / 2) << 23);
+        up1 = __uint_as_float((uint32_t)(127 + k - k / 2) << 23);
+    }
+    float ss = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < CH; ++i) {
+        s_chunk(me + i * width, f);
+        float part = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            f[j] = f[j] * up0 * up1;
+            part += f[j] * f[j];
+        }
+        if constexpr (CH < OC) chunk_sum[me + i * width] = part;
+        else ss += part;
+    }
+    const float mean = row_sum<CH, OC>(ss, chunk_sum, red, chunks) / (float)H + eps * up0 * up1 * up0 * up1;
+    const float rs = 1.0f / sqrtf(mean) * up1;   // rstd = rs up0
+    if (rstd_out && me == 0) *rstd_out = rs * up0;
+#pragma unroll 1
+    for (int i = 0; i < CH; ++i) {
+        const int c = me + i * width;
+        s_chunk(c, f);
+        if (c < chunks) {
+            float w[8];
+            unpack8(weight[c], w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = f[j] * up0 * rs * w[j];
+            if (y) y[c] = pack8(f);
+        }
+        if (y_q) {
+            uint2 q;
+            const uint32_t byte = rows8_quantize_quad(f, q);
+            if (c < chunks) {
+                *reinterpret_cast<uint2*>(y_q + 8 * c) = q;
+                if ((c & 3) == 0) y_scale[c >> 2] = (uint8_t)byte;
+            }
+        }
+    }
+}
+
 // Forward. One row per block, whose threads hold CH 8-column chunks each. The squares
 // are added in one order for a given H, so that a row's results do not depend on T, by
 // which CH is chosen: the eight of a chunk; W apart, the OC chunks of one of W sums; 32
@@ -71,7 +176,6 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
     static_assert(CH <= OC, "the order is the kernel's for many rows, whose threads hold more chunks");
     __shared__ float red[kMaxWarps];
     __shared__ float chunk_sum[CH < OC ? 32 * kMaxWarps * CH : 1];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int width = (int)blockDim.x, me = (int)threadIdx.x;
     const int64_t t = blockIdx.x;
     const int chunks = H / 8;
@@ -106,20 +210,15 @@ __global__ void __launch_bounds__(32 * kMaxWarps)
         if constexpr (CH < OC) chunk_sum[me + i * width] = part;   // absent chunks: 0
         else ss += part;
     }
-    int sums = width;   // W
-    if constexpr (CH < OC) {
-        sums = row_sums(chunks, OC);
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < OC; ++i)
-            if (me < sums && me + i * sums < chunks) ss += chunk_sum[me + i * sums];
+    const float mean = row_sum<CH, OC>(ss, chunk_sum, red, chunks) / (float)H + eps;
+    if (mean < kSmallestMean || mean == INFINITY) {   // the same in every thread
+        scaled_row<CH, OC>((sum ? sum : x) + t * chunks, residual && !sum ? residual + t * chunks : nullptr, weight, H,
+                           eps, y ? y + t * chunks : nullptr, y_q ? y_q + t * H : nullptr,
+                           y_q ? y_scale + t * rows8_blocks(H) : nullptr, rstd_out ? rstd_out + t : nullptr,
+                           chunk_sum, red);
+        return;
     }
-    ss = warp_sum(ss);
-    if (lane == 0) red[warp] = ss;
-    __syncthreads();
-    ss = 0.0f;
-    for (int i = 0; i < (sums >> 5); ++i) ss += red[i];
-    const float rstd = 1.0f / sqrtf(ss / (float)H + eps);
+    const float rstd = 1.0f / sqrtf(mean);
     if (rstd_out && me == 0) rstd_out[t] = rstd;
     const int S = rows8_blocks(H);
 #pragma unroll

@@ -36,3 +36,100 @@ def test_a_row_alone_and_in_a_batch(H):
     some = m.moe_rmsnorm_backward(r, many["sum"], w, many["rstd"])
     one = [m.moe_rmsnorm_backward(r[i:i + 1], a["sum"], w, a["rstd"]) for i, a in zip(rows, alone)]
     assert torch.equal(torch.cat([o["dx"] for o in one]), some["dx"][::3])
+
+
+SIZES = [-133, -130, -126, -110, -80, -75, -70, -63, -52, -50, -48, -20, 0, 30, 58, 63, 64, 90, 120, 126]
+
+
+# eps: none, the smallest fp32, one that counts for some of the small rows, usual ones
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -149, 2.0 ** -105, 1e-12, 1e-6])
+@pytest.mark.parametrize("H,copies", [(64, 1), (2048, 1), (2048, 20), (5120, 1), (5120, 20), (16384, 1)])
+def test_rows_of_every_size(H, copies, eps):
+    """Rows of sizes 2^-133 .. 2^126, whose squares leave fp32's range on either side."""
+    require_gpu()
+    import routing_grouped_gemm_score_b200 as m
+    x, dy, w = batch(len(SIZES), H, 2)
+    row = (x.float() / x.float().abs().amax(dim=1, keepdim=True)).double()   # magnitude 1
+    x = torch.stack([r * 2.0 ** e for r, e in zip(row, SIZES)]).to(torch.bfloat16).repeat(copies, 1)
+    dy = dy.repeat(copies, 1)
+    r = m.moe_rmsnorm(x, w, eps, quantize=True)
+    s, wd = x.double().cpu(), w.cpu().double()
+    y, rstd = ref.rmsnorm(s, wd, eps)
+    stored = rstd.float().double()   # as fp32 holds it: 2^-150 off where it is denormal, inf from 2^128 on
+    ref.assert_within(r["rstd"], stored, RSTD * stored + 2.0 ** -149, "rstd")
+    ref.assert_within(r["y"], y, (ref.BF16 + RSTD + 2 * ref.F32) * y.abs() + 2.0 ** -134, "y")
+    back = ref.decode(r["y_q"].cpu(), r["y_scale"].cpu())
+    unit = ref.per_column(torch.exp2(r["y_scale"].cpu().double() - 127), H)
+    d = RSTD + 2 * ref.F32
+    mag = ref.split_blocks(y.abs(), 1)[0].amax(dim=2)
+    lo, hi = ref.exponents(mag * (1 - d)) + 127, ref.exponents(mag * (1 + d)) + 127
+    assert bool(((r["y_scale"].cpu() >= lo) & (r["y_scale"].cpu() <= hi)).all())
+    ref.assert_within(back, y, (2.0 ** -4 * (1 + d) + d) * y.abs() + 2.0 ** -10 * unit, "y in 8 bits")
+    # the backward, which has rstd from the forward, where it is a number
+    ok = torch.isfinite(r["rstd"]).cpu()
+    g = m.moe_rmsnorm_backward(dy[ok.cuda()], x[ok.cuda()], w, r["rstd"][ok.cuda()])
+    s, dyd, rs = s[ok], dy.cpu().double()[ok], r["rstd"].cpu().double()[ok]
+    dx, dw = ref.rmsnorm_backward(dyd, s, wd, rs)
+    xhat = (s * rs[:, None]).abs()
+    c_abs = (wd * dyd * xhat).abs().sum(dim=1, keepdim=True) / H
+    terms = rs[:, None] * ((wd * dyd).abs() + xhat * c_abs)
+    tol = ref.BF16 * dx.abs() + 64 * ref.F32 * terms + 2.0 ** -134
+    got = g["dx"].cpu().double()
+    # rstd is up to 2^128, so some gradients pass bf16's largest value, 2^128 - 2^119, which is stored as an infinity
+    past = dx.abs() + tol >= torch.finfo(torch.bfloat16).max
+    ref.assert_within(got[~past], dx[~past], tol[~past], "dx")
+    assert bool(((got - dx).abs() <= tol)[past].logical_or(got[past] == dx[past].sign() * float("inf")).all())
+    n = int(ok.sum())
+    ref.assert_within(g["dweight"], dw, (n + 64 + 2) * ref.F32 * (dyd * xhat).abs().sum(dim=0) + 2.0 ** -130, "dweight")
+
+
+def test_zeros_infinities_and_one_large_value():
+    require_gpu()
+    import routing_grouped_gemm_score_b200 as m
+    H = 264
+    x, _, w = batch(8, H, 3)
+    x[0] = 0.0
+    x[1] = 0.0
+    x[1, 7] = 2.0 ** -133                                  # one value, the smallest
+    x[2] = 2.0 ** -120
+    x[2, 5] = 2.0 ** 126                                   # one that dwarfs the row
+    x[3, 5], x[4, 5] = float("inf"), float("nan")
+    x[5] = 3.3895e38
+    for eps in (0.0, EPS):
+        r = m.moe_rmsnorm(x, w, eps, quantize=True)
+        y, rstd = ref.rmsnorm(x.cpu().double(), w.cpu().double(), eps)
+        y[3], rstd[3] = 0.0, 0.0                           # finite values over an infinite length
+        y[3, 5] = float("nan")                             # inf / inf
+        stored = rstd.float().double()
+        ref.assert_within(r["rstd"], stored, RSTD * stored + 2.0 ** -149, "rstd")
+        ref.assert_within(r["y"], y, (ref.BF16 + RSTD + 2 * ref.F32) * y.abs() + 2.0 ** -134, "y")
+        if eps == 0.0:
+            assert torch.isnan(r["y"][0]).all()            # 0 / 0
+            assert float(r["y"][1, 7]) == float((w[7].float() * H ** 0.5).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("e", [-80, 70])
+@pytest.mark.parametrize("H", [264, 5120])
+def test_such_rows_with_a_residual_and_in_place(H, e):
+    """The path of these rows reads them again: from the sum, or from x and residual."""
+    require_gpu()
+    import routing_grouped_gemm_score_b200 as m
+    x, r, w = (t if t.dim() == 1 else (t.float() * 2.0 ** e).to(t.dtype) for t in batch(200, H, 4))
+    want = m.moe_rmsnorm(x, w, 0.0, residual=r, quantize=True)
+    s = (x.double() + r.double()).to(torch.bfloat16).double().cpu()
+    assert torch.equal(want["sum"].cpu().double(), s)
+    y, rstd = ref.rmsnorm(s, w.cpu().double(), 0.0)
+    ref.assert_within(want["rstd"], rstd, RSTD * rstd, "rstd")
+    ref.assert_within(want["y"], y, (ref.BF16 + RSTD + 2 * ref.F32) * y.abs(), "y")
+    for where in ({"sum": None}, {"sum": "x"}, {"sum": "r"}, {"y": "x"}, {"y": "x", "sum": None}, {"y": "x", "sum": "r"}):
+        c = {"x": x.clone(), "r": r.clone()}
+        got = m.moe_rmsnorm(c["x"], w, 0.0, residual=c["r"], quantize=True,
+                            out={n: c.get(t) for n, t in where.items()})
+        for n in want:
+            assert got[n] is None if where.get(n, n) is None else torch.equal(got[n], want[n]), (where, n)
+    c = want["sum"].clone()
+    got = m.moe_rmsnorm(c, w, 0.0, quantize=True, out={"y": c})
+    assert torch.equal(c, want["y"]) and torch.equal(got["y_q"], want["y_q"]) and torch.equal(got["rstd"], want["rstd"])
+    alone = m.moe_rmsnorm(x[8:9], w, 0.0, residual=r[8:9], quantize=True)
+    for n in want:
+        assert torch.equal(alone[n], want[n][8:9]), n
