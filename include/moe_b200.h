@@ -558,7 +558,9 @@ moe_status moe_layer_forward_ckpt(const float* logits, const moe_bf16* x, int64_
  *  dw_down out bf16 [E,I,H]; dprob out fp32 [T,k];
  *  workspace of moe_grouped_mlp_backward_ckpt_workspace_size(T, H, I, E, k) bytes,
  *  16-byte aligned. A row index outside [0, T k) is recorded as
- *  MOE_ERR_DEVICE_CHECK and its assignment skipped. T k + 15 min(E, T k), the rows
+ *  MOE_ERR_DEVICE_CHECK and its assignment skipped: it has no part in any gradient,
+ *  and its dprob is 0. An index that two assignments have is recorded too; what
+ *  those two add to the gradients is then undefined. T k + 15 min(E, T k), the rows
  *  of its padded blocks, must be below 2^31 (MOE_ERR_UNSUPPORTED). */
 size_t moe_grouped_mlp_backward_ckpt_workspace_size(int64_t T, int H, int I, int E, int k);
 moe_status moe_grouped_mlp_backward_ckpt(const moe_bf16* dout, int64_t T, int H, int I, int E, int k,

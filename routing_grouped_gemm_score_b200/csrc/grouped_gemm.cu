@@ -124,6 +124,11 @@ struct Params {
     // of gu8. Row r of block g has g and u if r - offsets[g] < gu8_offsets[g + 1] -
     // gu8_offsets[g]; the others are zero rows
     const int32_t* gu8_offsets;
+    // kEpiSwigluBwd8: row r of A is assignment row_from[r]'s if pad_row[row_from[r]] = r;
+    // otherwise no assignment's: A's row is set to zeros (a_rows)
+    const int32_t* row_from;
+    const int32_t* pad_row;
+    bf16* a_rows;
     int I;                     // SwiGLU: offset of the up half in [g | u]
     int tma_out, tma_out2;     // single-CTA kernel: out / out2 have TMA store maps
     const float* row_scale;    // SwiGLU forward: h[r] *= row_scale[r]; backward: ds = row_scale[r] * dh (NULL: 1)
@@ -508,6 +513,13 @@ struct EpiAux<kEpiSwigluBwd8> {
         int64_t row;   // of gu8, -1: a row past the block or a zero row
     };
 };
+// A row of A that is no assignment's: recorded, and set to zeros for the products to come
+// (those of this launch that read it give rows that are not stored).
+__device__ __noinline__ void clear_row(bf16* row, int cols, unsigned* err) {
+    raise_error(err, kErrDeviceCheck);
+    for (int c = 0; c < cols; c += 8) *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+}
+
 template <int EPI>
 __device__ __forceinline__ void load_epi_aux(const Params& p, const Tile& t, int r, int col,
                                              typename EpiAux<EPI>::type& a) {
@@ -517,6 +529,13 @@ __device__ __forceinline__ void load_epi_aux(const Params& p, const Tile& t, int
         const int begin = __ldg(p.gu8_offsets + t.g), end = __ldg(p.gu8_offsets + t.g + 1);
         const int64_t row = (int64_t)begin + (t.row0 - t.first) + r;
         a.row = r < t.rows && row >= 0 && row < end && row < p.gu8_rows ? row : -1;
+        if (a.row >= 0) {
+            const int32_t from = __ldg(p.row_from + t.row0 + r);   // anything, if no assignment wrote it
+            if (from < 0 || from >= p.gu8_rows || __ldg(p.pad_row + from) != t.row0 + r) {
+                a.row = -1;
+                if (t.n_blk == 0) clear_row(p.a_rows + ((int64_t)t.row0 + r) * p.K, p.K, p.err);
+            }
+        }
         load_aux8(p, a.row, col, a.row >= 0 && col < p.N, a.a);
     }
 }
@@ -2616,10 +2635,10 @@ cudaError_t gemm_down_dgrad_swiglu(const bf16* dy, int64_t rows, const int32_t* 
     return launch_group_m<kEpiSwigluBwd, false>(ta, ta64, tb, tb1, p, st, &tc);
 }
 
-cudaError_t gemm_down_dgrad_swiglu8(const bf16* dy, int64_t rows, const int32_t* offsets, int E, int H, int I,
+cudaError_t gemm_down_dgrad_swiglu8(bf16* dy, int64_t rows, const int32_t* offsets, int E, int H, int I,
                                     const bf16* w_down, const Rows8& gu8, int64_t gu8_rows, const int32_t* gu8_offsets,
-                                    const float* row_scale, bf16* dgu, bf16* h, float* row_dot, cudaStream_t st,
-                                    unsigned* err) {
+                                    const int32_t* row_from, const int32_t* pad_row, const float* row_scale, bf16* dgu,
+                                    bf16* h, float* row_dot, cudaStream_t st, unsigned* err) {
     if (rows == 0) return cudaSuccess;
     CUtensorMap ta, ta64, tb, tb1;   // as in gemm_down_dgrad_swiglu
     if (!make_map_2d(&ta, dy, H, rows, H, BK, 128)) return cudaErrorInvalidValue;
@@ -2639,6 +2658,9 @@ cudaError_t gemm_down_dgrad_swiglu8(const bf16* dy, int64_t rows, const int32_t*
     p.gu8_scale = gu8.scale;
     p.gu8_rows = gu8_rows;
     p.gu8_offsets = gu8_offsets;
+    p.row_from = row_from;
+    p.pad_row = pad_row;
+    p.a_rows = dy;
     p.row_scale = row_scale;
     p.row_dot = row_dot;
     p.ld_row_dot = (I + 63) / 64;

@@ -154,7 +154,7 @@ struct Bwd8Layout {
     int64_t R;
     bf16 *rows, *dgu, *h;
     float *prob_row, *row_dot;
-    int32_t *pad_offsets, *pad_row;
+    int32_t *pad_offsets, *pad_row, *row_from;
     size_t bytes;
 };
 
@@ -169,6 +169,7 @@ Bwd8Layout bwd8_layout(void* ws, int64_t T, int H, int I, int E, int k) {
     L.row_dot = c.take<float>((size_t)L.R * ((I + 63) / 64));
     L.pad_offsets = c.take<int32_t>((size_t)E + 1);
     L.pad_row = c.take<int32_t>((size_t)(T * k));
+    L.row_from = c.take<int32_t>((size_t)L.R);
     L.bytes = c.bytes();
     return L;
 }
@@ -881,11 +882,11 @@ moe_status moe_grouped_mlp_backward_ckpt(const moe_bf16* dout, int64_t T, int H,
     cudaError_t e = trace_mark(0, st);
     if (e == cudaSuccess)
         e = launch_spread_rows(B(dout), row_of, offsets, topk_prob, T, k, E, H, L.rows, L.prob_row, L.pad_offsets,
-                               L.pad_row, st, err);
+                               L.pad_row, L.row_from, st, err);
     if (e == cudaSuccess) e = trace_mark(1, st);
     if (e == cudaSuccess)
-        e = gemm_down_dgrad_swiglu8(L.rows, L.R, blocks, E, H, I, B(w_down), gu8, A, offsets, L.prob_row, L.dgu, L.h,
-                                    L.row_dot, st, err);
+        e = gemm_down_dgrad_swiglu8(L.rows, L.R, blocks, E, H, I, B(w_down), gu8, A, offsets, L.row_from, L.pad_row,
+                                    L.prob_row, L.dgu, L.h, L.row_dot, st, err);
     if (e == cudaSuccess) e = trace_mark(2, st);
     if (e == cudaSuccess)
         e = gemm_wgrad(L.h, L.rows, L.R, blocks, E, I, H, reinterpret_cast<bf16*>(dw_down), st, err, true);

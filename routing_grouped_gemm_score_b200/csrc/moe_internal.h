@@ -172,10 +172,11 @@ cudaError_t launch_dequantize_rows(const uint8_t* q, const uint8_t* scale, int64
 // the first) hold the blocks and each assignment's row. rows has A + 15 min(E, A)
 // rows (pad16_rows).
 constexpr int64_t pad16_rows(int64_t A, int E) { return A + 15 * (A < E ? A : (int64_t)E); }
-// rows[pad_row[t, j]] = src[t], prob_row[row] = prob[t, j] (0 in a zero row)
+// rows[pad_row[t, j]] = src[t], prob_row[row] = prob[t, j] (0 in a zero row), and
+// row_from[row] = t k + j, not written in rows that no assignment has
 cudaError_t launch_spread_rows(const bf16* src, const int32_t* row_of, const int32_t* offsets, const float* prob,
                                int64_t T, int k, int E, int H, bf16* rows, float* prob_row, int32_t* pad_offsets,
-                               int32_t* pad_row, cudaStream_t st, unsigned* err);
+                               int32_t* pad_row, int32_t* row_from, cudaStream_t st, unsigned* err);
 // What is left to do by token between the gate_up dgrad and its weight's gradient,
 // with pad_row given: dx[t] = sum_j rows[pad_row[t, j]] (each row's dx), then those
 // rows become x[t], read back from x8 (the padding zeros); and dprob[t, j] = the sum
@@ -253,11 +254,13 @@ cudaError_t gemm_down_dgrad_swiglu(const bf16* dy, int64_t rows, const int32_t* 
 // gemm_down_dgrad_swiglu with row_scale and row_dot, and h[r] = row_scale[r] *
 // silu(g) * u, recomputed, for the down weight's gradient. The row blocks of dy and
 // of the outputs (offsets) may be padded; gu8's rows are those of gu8_offsets,
-// gu8_rows of them, and the rows past them in a block get zeros.
-cudaError_t gemm_down_dgrad_swiglu8(const bf16* dy, int64_t rows, const int32_t* offsets, int E, int H, int I,
+// gu8_rows of them, and the rows past them in a block get zeros. So does a row r that no
+// assignment has, pad_row[row_from[r]] != r (see launch_spread_rows): it is recorded
+// as kErrDeviceCheck, and its dy, which holds anything, is set to zeros as well.
+cudaError_t gemm_down_dgrad_swiglu8(bf16* dy, int64_t rows, const int32_t* offsets, int E, int H, int I,
                                     const bf16* w_down, const Rows8& gu8, int64_t gu8_rows, const int32_t* gu8_offsets,
-                                    const float* row_scale, bf16* dgu, bf16* h, float* row_dot, cudaStream_t st,
-                                    unsigned* err);
+                                    const int32_t* row_from, const int32_t* pad_row, const float* row_scale, bf16* dgu,
+                                    bf16* h, float* row_dot, cudaStream_t st, unsigned* err);
 // dgrad of gate_up: dx_perm = dgu Wgu[e]^T
 cudaError_t gemm_gate_up_dgrad(const bf16* dgu, int64_t rows, const int32_t* offsets, int E, int H,
                                int I, const bf16* w_gate_up, bf16* dx_perm, cudaStream_t st,

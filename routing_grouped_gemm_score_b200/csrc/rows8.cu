@@ -164,14 +164,17 @@ __device__ __forceinline__ void zero_pad_rows(const PadBlocks& b, int E, int chu
 // read once. A warp owns a unit of one token's row (512 columns); lane j finds the
 // row of assignment j: the expert of row_of[t, j] by bisection of the blocks' offsets,
 // then its place in the padded block. The unit of a token's first columns writes
-// pad_row and prob_row, and the first block pad_offsets. A row outside its range
-// is recorded and skipped (pad_row -1). 4096 tokens of 2048 columns, k = 8: 25-29 us
+// pad_row, prob_row and row_from, and the first block pad_offsets. A row outside its
+// range is recorded and skipped (pad_row -1). A row of a block that no assignment has
+// keeps what the memory held: the down dgrad finds those rows, by a row_from whose
+// pad_row is another, and clears them. 4096 tokens of 2048 columns, k = 8: 25-29 us
 // (134 MB written), 8192 of 5120, k = 1: 31 us (84 MB read, 84 written).
 __global__ void __launch_bounds__(kThreads)
     spread_rows_kernel(const uint4* __restrict__ src, const int32_t* __restrict__ row_of,
                        const int32_t* __restrict__ offsets, const float* __restrict__ prob, int64_t T, int k, int E,
                        int H, uint4* __restrict__ rows, float* __restrict__ prob_row,
-                       int32_t* __restrict__ pad_offsets, int32_t* __restrict__ pad_row, unsigned* err) {
+                       int32_t* __restrict__ pad_offsets, int32_t* __restrict__ pad_row,
+                       int32_t* __restrict__ row_from, unsigned* err) {
     __shared__ PadBlocks b;
     pdl_wait();
     pdl_launch_dependents();
@@ -203,7 +206,10 @@ __global__ void __launch_bounds__(kThreads)
             if (mine < 0) raise_error(err, kErrDeviceCheck);
             if (part == 0) {
                 pad_row[t * k + lane] = mine;
-                if (mine >= 0) prob_row[mine] = __ldg(prob + t * k + lane);
+                if (mine >= 0) {
+                    prob_row[mine] = __ldg(prob + t * k + lane);
+                    row_from[mine] = (int32_t)(t * k + lane);
+                }
             }
         }
         uint4 v[kSpreadChunks];
@@ -349,12 +355,12 @@ cudaError_t launch_dequantize_rows(const uint8_t* q, const uint8_t* scale, int64
 
 cudaError_t launch_spread_rows(const bf16* src, const int32_t* row_of, const int32_t* offsets, const float* prob,
                                int64_t T, int k, int E, int H, bf16* rows, float* prob_row, int32_t* pad_offsets,
-                               int32_t* pad_row, cudaStream_t st, unsigned* err) {
+                               int32_t* pad_row, int32_t* row_from, cudaStream_t st, unsigned* err) {
     if (T == 0) return cudaSuccess;
     const int64_t units = T * ((H / 8 + kSpreadUnit - 1) / kSpreadUnit);
     return launch_chained(spread_rows_kernel, dim3(unit_blocks(units, resident_blocks())), dim3(kThreads), 0, st,
                           reinterpret_cast<const uint4*>(src), row_of, offsets, prob, T, k, E, H,
-                          reinterpret_cast<uint4*>(rows), prob_row, pad_offsets, pad_row, err);
+                          reinterpret_cast<uint4*>(rows), prob_row, pad_offsets, pad_row, row_from, err);
 }
 
 cudaError_t launch_finish_rows(const Rows8& x8, const int32_t* offsets, int64_t T, int k, int E, int H, bf16* rows,
