@@ -133,3 +133,39 @@ def test_such_rows_with_a_residual_and_in_place(H, e):
     alone = m.moe_rmsnorm(x[8:9], w, 0.0, residual=r[8:9], quantize=True)
     for n in want:
         assert torch.equal(alone[n], want[n][8:9]), n
+
+
+@pytest.mark.parametrize("H", [72, 512, 4096])
+def test_gradient_against_differences_of_the_kernel_itself(H):
+    """<dx, v> of the backward kernel against (L(s + h v) - L(s - h v)) / 2h with
+    L(s) = <dy, w s rstd>, rstd from the forward kernel (fp32; y in bf16 is too coarse),
+    the rest in 64 bits. s has multiples of h = 2^-6 below 2, and v signs, so that the
+    three rows are bf16 numbers. v takes the signs of the formula's gradient, so <dx, v> is
+    the sum of its magnitudes: far above the tolerance, which a dx of zeros would miss."""
+    require_gpu()
+    import routing_grouped_gemm_score_b200 as m
+    T, h = 5, 2.0 ** -6
+    g = torch.Generator().manual_seed(H)
+    s = torch.randint(-126, 127, (T, H), generator=g).double() * h
+    dy = torch.randn(T, H, generator=g).to(torch.bfloat16)
+    w = (1 + 0.3 * torch.randn(H, generator=g)).to(torch.bfloat16)
+    dyw, wd = dy.double() * w.double(), w.double()
+    v = ref.rmsnorm_backward(dy.double(), s, wd, ref.rmsnorm(s, wd, EPS)[1])[0].sign()
+    rows = [(s + k * h * v).to(torch.bfloat16) for k in (0, 1, -1)]
+    assert all(torch.equal(r.double(), s + k * h * v) for r, k in zip(rows, (0, 1, -1)))
+    rstd = [m.moe_rmsnorm(r.cuda(), w.cuda(), EPS)["rstd"] for r in rows]
+    loss = lambda r, rs: (dyw * r.double()).sum(dim=1) * rs.double().cpu()  # noqa: E731
+    up, down = loss(rows[1], rstd[1]), loss(rows[2], rstd[2])
+    got = m.moe_rmsnorm_backward(dy.cuda(), rows[0].cuda(), w.cuda(), rstd[0])["dx"].double().cpu()
+    along = (got * v).sum(dim=1)
+    # the difference's own error, h^2 L''' / 6 and more: the formula's difference less its derivative, in 64 bits
+    exact = lambda k: loss(s + k * h * v, ref.rmsnorm(s + k * h * v, wd, EPS)[1])  # noqa: E731
+    dx = ref.rmsnorm_backward(dy.double(), s, wd, ref.rmsnorm(s, wd, EPS)[1])[0]
+    cut = ((exact(1) - exact(-1)) / (2 * h) - (dx * v).sum(dim=1)).abs()
+    xhat = s * rstd[0].double().cpu()[:, None]
+    terms = rstd[0].double().cpu()[:, None] * (dyw.abs() + xhat.abs() * (dyw * xhat).abs().sum(dim=1, keepdim=True) / H)
+    # rstd of the two rows; dx to bf16 and its fp32 terms, as in test_backward; rstd of s enters dx twice
+    tol = cut + RSTD * (up.abs() + down.abs()) / (2 * h) + ref.BF16 * dx.abs().sum(dim=1) + (
+        64 * ref.F32 + 3 * RSTD) * terms.sum(dim=1)
+    assert bool((along > 20 * tol).all())
+    assert bool(((up - down) / (2 * h) - along).abs().le(tol).all())
