@@ -548,7 +548,8 @@ __device__ __forceinline__ void load_epi_aux(const Params& p, const Tile& t, int
 // The sigmoid takes the intrinsics: __expf(x) is off by at most 2 + 1.173 |x| ulp and
 // __fdividef by 2, thousands of times less than the 2^-4 that g and u are held
 // to. With expf and __frcp_rn this epilogue bounds the GEMM (Qwen3-30B-A3B: 186
-// against 158 us, and 155 without any sigmoid). Where __expf overflows (g < -88)
+// against 158 us, and 155 without any sigmoid; 161 with the rows' check in load_epi_aux
+// today). Where __expf overflows (g < -88)
 // the quotient is 0, the sigmoid's value there.
 __device__ __forceinline__ void swiglu_bwd8(const float* dh, const Aux8& a, float p, float& dot, uint32_t* dgp,
                                             uint32_t* dup, uint32_t* hp) {
@@ -1405,10 +1406,10 @@ __global__ void __launch_bounds__(GROUP_K ? kThreadsK : kThreads, 1)
 // barrier. Without the padding, each expert's last slice had to pass through a
 // warp per CTA that zeroed the rows past its end and released them to the
 // leader: about 1 us a tile, 274 against 262 us of the single-CTA kernel for the
-// Qwen3-30B-A3B gate_up gradient (231 padded; Llama-4: 1168 against 1302).
+// Qwen3-30B-A3B gate_up gradient (padded: 241 against 262; Llama-4: 1204 against 1340).
 // What bounds it (timed in parts, Qwen3-30B-A3B): loads alone take 147 us, MMAs alone
 // 169, the epilogue with its stores 147; nothing is saturated (ncu: DRAM 51 %,
-// tensor pipe 40 %, L2 reads 30 %), so the rest is the latency between the roles
+// tensor pipe 44 %, L2 reads 24 %), so the rest is the latency between the roles
 // on tiles of four K slices.
 // Shared memory of gemm_wgrad_pair_kernel: a ring of 5 stages, and two store
 // buffers of 32 rows x 64 columns per epilogue warp, so that a tile's stores have
@@ -2343,11 +2344,12 @@ bool use_swap_tiles(int64_t rows, int groups) {
 }
 
 // Weight gradients on CTA pairs (row blocks padded to 16): for more output rows than
-// one CTA's 128, and from 128 rows per expert on. Measured, pair against single
-// tiles, dW_down + dW_gate_up: Qwen3-30B-A3B widths, 32 rows per expert 104 + 182
-// against 96 + 163 us, 128 rows 92 + 171 against 97 + 181, 256 rows 125 + 231
-// against 136 + 251; Mixtral widths, 16 rows 204 + 370 against 175 + 328, 128 rows
-// 363 + 414 against 368 + 430. With few K slices a tile is all hand-over.
+// one CTA's 128, and from 128 rows per expert on, the padding counted. Measured, pair
+// against single tiles, dW_down + dW_gate_up: Qwen3-30B-A3B widths, 32 rows per expert
+// 98 + 170 against 99 + 158 us, 128 rows 91 + 172 against 97 + 182, 256 rows 129 + 244
+// against 140 + 262; Mixtral widths, 16 rows 215 + 371 against 190 + 335, 128 rows
+// 233 + 418 against 255 + 427; Llama-4, 512 rows 616 + 1205 against 686 + 1339. With few
+// K slices a tile is all hand-over.
 bool use_pair_wgrad(int64_t rows, int groups, int M) {
     const int forced = kernel_override().gemm_tiles;
     if (forced != MOE_TESTING_AUTO) return forced == MOE_TESTING_GEMM_PAIR;

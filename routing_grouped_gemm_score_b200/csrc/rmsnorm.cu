@@ -13,7 +13,7 @@
 // read once, stays in registers (forward) or in shared memory (backward) until its
 // sum is known, and is written once. Measured: 16384 rows of 5120 with a residual
 // and both outputs 122 us (6.2 TB/s), their backward for 8192 rows 59 + 5 us for
-// dweight (5.7 TB/s); one row of 2048 2.2 us.
+// dweight (5.7 TB/s); one row of 2048 2.1-2.3 us.
 #include "moe_internal.h"
 #include "rows8.cuh"
 

@@ -167,8 +167,8 @@ __device__ __forceinline__ void zero_pad_rows(const PadBlocks& b, int E, int chu
 // pad_row, prob_row and row_from, and the first block pad_offsets. A row outside its
 // range is recorded and skipped (pad_row -1). A row of a block that no assignment has
 // keeps what the memory held: the down dgrad finds those rows, by a row_from whose
-// pad_row is another, and clears them. 4096 tokens of 2048 columns, k = 8: 25-29 us
-// (134 MB written), 8192 of 5120, k = 1: 31 us (84 MB read, 84 written).
+// pad_row is another, and clears them. 4096 tokens of 2048 columns, k = 8: 30 us
+// (134 MB written), 8192 of 5120, k = 1: 32 us (84 MB read, 84 written).
 __global__ void __launch_bounds__(kThreads)
     spread_rows_kernel(const uint4* __restrict__ src, const int32_t* __restrict__ row_of,
                        const int32_t* __restrict__ offsets, const float* __restrict__ prob, int64_t T, int k, int E,
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads)
 // of a column chunk are issued together. The unit of a token's first columns also
 // sums its routing weights' gradients: the 32 / KB lanes of an assignment take
 // every so many-th partial, a butterfly adds theirs, a fixed order.
-// In one launch for k = 8 (4096 x 2048) 54 us, for k = 1 (8192 x 5120) 51; as three (the
+// In one launch for k = 8 (4096 x 2048) 54 us, for k = 1 (8192 x 5120) 50; as three (the
 // token sum, the weights' sums, x by row) 27 + 4 + 26 and 30 + 5 + 27.
 template <int KB, int CH>
 __global__ void __launch_bounds__(kThreads, KB > 8 ? 2 : 4)
